@@ -1,0 +1,277 @@
+// Appending keys and values to the paged 8-bit cache, with the keys' norm and
+// rotation on the way (rope.cuh, cache.cuh).
+//
+// The work is cut by pages: a unit is the new tokens of one sequence that fall
+// in one page, and a unit's K or V of one kv-head is quantised as a whole,
+// because its scale is the largest exponent among them.  Sequence s owns the
+// unit numbers floor(new_start[s] / page) + 2 s and up; it touches at most
+// floor(tokens / page) + 2 pages, so the ranges never meet, and a warp finds
+// its sequence by a 32-way search without a pass over the lengths.
+//
+// Two kernels, by the tokens per sequence (see launch_cache_append): a block
+// per (unit, kv-head, K or V) that keeps the page's tokens in registers
+// between the maximum and the rounding (each element is read once), and, for
+// decode steps, a warp per (unit, kv-head, K or V).  Bytes bound the first,
+// launch and the chain of dependent index loads the second.
+#include <cuda_bf16.h>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "rope.cuh"
+
+namespace ssa {
+namespace {
+
+struct AppendCfg {
+  AppendArgs g;
+  int64_t k_stride, v_stride;
+  int32_t n_tokens, n_seq, max_pages, n_pages, h_kv, rot, layout, norm;
+  int32_t n_units;
+  float eps, mscale;
+};
+
+struct AppendUnit {
+  int32_t t0, n;       // new tokens (rows of K and V)
+  int32_t slot0;       // slot of the first
+  int32_t pos0;        // its position
+  int32_t page;        // -1: nothing to do
+};
+
+// All lanes of the warp get the unit; `count` (one caller per unit) adds what
+// is left out to the bad counter.
+template <int P>
+__device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t unit, bool count) {
+  const int lane = threadIdx.x & 31;
+  AppendUnit u;
+  u.page = -1;
+  u.n = 0;
+  const auto start = [&](int s) { return min(max(__ldg(a.g.new_start + s), 0), a.n_tokens); };
+  int lo = 0, hi = a.n_seq;   // the sequence is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const bool le = s < hi && start(s) / P + 2 * static_cast<int64_t>(s) <= unit;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    if (n == 0) return u;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int a0 = start(lo), a1 = max(start(lo + 1), a0);
+  const int64_t j = unit - (a0 / P + 2 * static_cast<int64_t>(lo));
+  const int have = __ldg(a.g.cached + lo);
+  if (j < 0 || a1 == a0) return u;
+  if (have < 0) {
+    if (count && j == 0 && lane == 0 && a.g.bad) atomicAdd(a.g.bad, a1 - a0);
+    return u;
+  }
+  const int64_t pi = have / P + j;
+  const int64_t p0 = max(static_cast<int64_t>(have), pi * P);
+  const int64_t p1 = min(static_cast<int64_t>(have) + (a1 - a0), (pi + 1) * P);
+  if (p1 <= p0) return u;
+  const int n = static_cast<int>(p1 - p0);
+  const int page = pi < a.max_pages ? __ldg(a.g.table + static_cast<int64_t>(lo) * a.max_pages + pi) : -1;
+  if (page < 0 || page >= a.n_pages) {
+    if (count && lane == 0 && a.g.bad) atomicAdd(a.g.bad, n);
+    return u;
+  }
+  u.n = n;
+  u.t0 = a0 + static_cast<int>(p0 - have);
+  u.slot0 = static_cast<int>(p0 - pi * P);
+  u.pos0 = static_cast<int>(p0);
+  u.page = page;
+  return u;
+}
+
+__device__ __forceinline__ float finite_amax(const float (&x)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = fabsf(x[i]);
+    m = v <= 3.402823466e38f ? fmaxf(m, v) : m;   // infinities and NaN left out
+  }
+  return m;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[8], float inv) {
+  uint2 w;
+  w.x = to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+  w.y = to_e4m3x2(x[4] * inv, x[5] * inv) | to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+// Rounds 16 codes again to a scale 2^-down times coarser.
+__device__ __forceinline__ void round_again(uint8_t* p, float down) {
+  uint4 v = *reinterpret_cast<uint4*>(p);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t hb = e4m3x2_to_half2(w[i] >> (16 * k) & 0xFFFFu);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hb));
+      out |= to_e4m3x2(f.x * down, f.y * down) << (16 * k);
+    }
+    w[i] = out;
+  }
+  *reinterpret_cast<uint4*>(p) = v;
+}
+
+// One row's eight dims of this lane in float32: the key normed and rotated,
+// the value as it is.
+template <typename T, int LPR, bool PRECISE>
+__device__ __forceinline__ void append_row(const AppendCfg& a, bool is_k, const Row8<T>& r, const float (&w)[8],
+                                           const uint64_t (&phase)[8], int sub, int lane, int pos, float (&x)[8]) {
+  r.get(x);
+  if (!is_k) return;
+  if (a.norm) norm_row<LPR>(x, w, a.eps);
+  if (a.rot > 0) {
+    Turn<PRECISE> t;
+    t.set(phase, sub, a.rot, a.layout, pos, a.mscale);
+    t.apply(x, a.layout, lane, 8 * sub < a.rot);
+  }
+}
+
+// The page's exponent, and the rounding of what it held when that grows.
+template <int D>
+__device__ __forceinline__ int page_exponent(const AppendUnit& u, float amax, float* scale, uint8_t* codes, int thread,
+                                             int threads) {
+  const int e_new = scale_exponent(amax);
+  if (u.slot0 == 0) return e_new;
+  const int e_old = exponent_of(*scale);
+  if (e_new <= e_old) return e_old;
+  const float down = pow2(e_old - e_new);
+  for (int i = thread; i < u.slot0 * (D / 16); i += threads) round_again(codes + i * 16, down);
+  return e_new;
+}
+
+// Prompts: a block per (unit, kv-head, K or V), the page's rows in registers.
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(256) append_page_kernel(const AppendCfg a) {
+  constexpr int LPR = D / 8, ROWS = 256 / LPR, KEEP = P / ROWS;
+  __shared__ float red[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, sub = lane % LPR;
+  const int row = threadIdx.x / LPR;
+  const int head = blockIdx.x % a.h_kv;
+  const int64_t unit = blockIdx.x / a.h_kv;
+  const bool is_k = blockIdx.y == 0;
+  const AppendUnit u = append_unit<P>(a, unit, head == 0 && is_k && warp == 0);
+  if (u.page < 0) return;
+  const T* src = is_k ? static_cast<const T*>(a.g.K) + static_cast<int64_t>(u.t0) * a.k_stride
+                      : static_cast<const T*>(a.g.V) + static_cast<int64_t>(u.t0) * a.v_stride;
+  const int64_t stride = is_k ? a.k_stride : a.v_stride;
+  src += static_cast<int64_t>(head) * D + 8 * sub;
+  Row8<T> r[KEEP];
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) r[k].load(src + static_cast<int64_t>(min(row + k * ROWS, u.n - 1)) * stride);
+  float w[8];
+  uint64_t phase[8];
+  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, sub, w);
+  lane_phases(a.g.freq, sub, is_k ? a.rot : 0, a.layout, phase);
+  float x[KEEP][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {   // rows past the last repeat it: the same maximum
+    append_row<T, LPR, sizeof(T) == 4>(a, is_k, r[k], w, phase, sub, lane, u.pos0 + min(row + k * ROWS, u.n - 1), x[k]);
+    amax = finite_amax(x[k], amax);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
+  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + head;
+  uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
+  float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
+  const int e = page_exponent<D>(u, amax, scale, codes, threadIdx.x, 256);
+  const float inv = pow2(-e);
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k)
+    if (row + k * ROWS < u.n) store_codes(codes + (u.slot0 + row + k * ROWS) * D + 8 * sub, x[k], inv);
+  __syncthreads();   // every thread has read the old scale
+  if (threadIdx.x == 0) *scale = pow2(e);
+}
+
+// Decode steps: a warp per (unit, kv-head, K or V).  More rows than one pass
+// holds are read twice.
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane % LPR, row = lane / LPR;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  const int64_t unit = item / (2 * a.h_kv);
+  if (unit >= a.n_units) return;
+  const int hk = static_cast<int>(item % (2 * a.h_kv));
+  const bool is_k = hk < a.h_kv;
+  const int head = is_k ? hk : hk - a.h_kv;
+  const AppendUnit u = append_unit<P>(a, unit, hk == 0);
+  if (u.page < 0) return;
+  const int64_t stride = is_k ? a.k_stride : a.v_stride;
+  const T* src = static_cast<const T*>(is_k ? a.g.K : a.g.V) + static_cast<int64_t>(u.t0) * stride +
+                 static_cast<int64_t>(head) * D + 8 * sub;
+  float w[8];
+  uint64_t phase[8];
+  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, sub, w);
+  lane_phases(a.g.freq, sub, is_k ? a.rot : 0, a.layout, phase);
+  float x[8];
+  const auto value = [&](int i0) {
+    const int i = min(i0 + row, u.n - 1);
+    Row8<T> r;
+    r.load(src + static_cast<int64_t>(i) * stride);
+    append_row<T, LPR, sizeof(T) == 4>(a, is_k, r, w, phase, sub, lane, u.pos0 + i, x);
+  };
+  float amax = 0.f;
+  for (int i0 = 0; i0 < u.n; i0 += RPW) {
+    value(i0);
+    amax = finite_amax(x, amax);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + head;
+  uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
+  float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
+  const int e = page_exponent<D>(u, amax, scale, codes, lane, 32);
+  const float inv = pow2(-e);
+  for (int i0 = 0; i0 < u.n; i0 += RPW) {
+    if (u.n > RPW) value(i0);
+    if (i0 + row < u.n) store_codes(codes + (u.slot0 + i0 + row) * D + 8 * sub, x, inv);
+  }
+  __syncwarp();
+  if (lane == 0) *scale = pow2(e);
+}
+
+template <typename T, int D, int P>
+cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
+  const int64_t units = a.n_tokens / P + 2 * static_cast<int64_t>(a.n_seq);
+  if (units > INT32_MAX || units * a.h_kv > INT32_MAX) return cudaErrorInvalidValue;
+  a.n_units = static_cast<int32_t>(units);
+  if (a.n_tokens <= 16 * static_cast<int64_t>(a.n_seq)) {
+    const int64_t grid = (units * 2 * a.h_kv + 7) / 8;
+    append_few_kernel<T, D, P><<<static_cast<unsigned>(grid), 256, 0, c.stream>>>(a);
+  } else {
+    const dim3 grid(static_cast<unsigned>(units * a.h_kv), 2);
+    append_page_kernel<T, D, P><<<grid, 256, 0, c.stream>>>(a);
+  }
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pick_append(const ssa_append_params& p, const AppendCfg& a, const LaunchCtx& c) {
+  if (p.d == 128) return p.page == 64 ? run_append<T, 128, 64>(a, c) : run_append<T, 128, 128>(a, c);
+  return p.page == 64 ? run_append<T, 64, 64>(a, c) : run_append<T, 64, 128>(a, c);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const ssa_append_params& p, const AppendArgs& g, const LaunchCtx& c) {
+  AppendCfg a{};
+  a.g = g;
+  a.k_stride = p.k_stride; a.v_stride = p.v_stride;
+  a.n_tokens = p.n_tokens; a.n_seq = p.n_seq; a.max_pages = p.max_pages; a.n_pages = p.n_pages;
+  a.h_kv = p.h_kv; a.rot = p.rot; a.layout = p.layout; a.norm = p.norm;
+  a.eps = p.eps; a.mscale = p.mscale;
+  return p.dtype == SSA_BF16 ? pick_append<__nv_bfloat16>(p, a, c) : pick_append<float>(p, a, c);
+}
+
+}  // namespace ssa

@@ -1,0 +1,613 @@
+// Attention of new tokens over the paged 8-bit cache, all keys or the
+// selected blocks plus the window.
+//
+// A unit is up to 16 query rows that share a kv-head (new tokens x the G query
+// heads of the group; with selected blocks one token's G heads), the M = 16
+// rows of a warp's m16n8k16 products, and a unit's keys are cut into `splits`
+// runs, one block each, whose partial results a second kernel joins.  Each of
+// a block's four warps walks its own 32-key pieces (every fourth of the run)
+// with a ring of bulk copies of its own, so no warp waits for another until
+// the end.  The products are small against the bytes (2 G flops per byte):
+// this kernel is bound by reading codes, and what it does per code counts:
+//
+//  * codes become float16 (exact) straight from shared memory to the B
+//    operands, without a pass through float32.  The k index of a product may
+//    run over the dims (or keys) in any order as long as both operands agree,
+//    so a lane takes 16 consecutive bytes of a key (S) or of a value row (P V)
+//    and calls them its k indexes; for P V, bytes of two keys are paired by
+//    byte permutes before the conversion.
+//  * a page's key scale multiplies its logits; its value scale 2^e is added to
+//    the base-2 logits: P' = 2^(s + e - M), M the running maximum of s + e,
+//    is at most 1, fits float16 and needs no factor on the output, and the sum
+//    of the softmax takes P' 2^-e.
+//  * queries become float16 after scaling each row by a power of two to a
+//    largest element in [2^14, 2^15): exact down to 2^-29 of the largest.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "cache.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "tiles.cuh"
+
+namespace ssa {
+namespace {
+
+constexpr int kPiece = 32;     // keys per piece
+constexpr int kWarps = 4;
+constexpr int kMaxEnt = 32 + 4032 / 64 + 2;   // selected blocks and window blocks
+constexpr int kSmCount = 148;
+
+struct CacheCfg {
+  CacheAttnArgs g;
+  int32_t n_seq, n_q, max_pages, n_pages, page, h_q, h_kv, G, topk, window;
+  int32_t tiles;     // units per (sequence, kv-head)
+  int32_t rows;      // partial rows stored per unit
+  int32_t splits;
+  float scale_log2;
+  float* part_o;     // [units][splits][rows][D]
+  float2* part_ml;   // [units][splits][rows]: running maximum, sum
+  uint32_t* err;
+};
+
+template <int D>
+struct CacheShape {
+  static constexpr int K_BYTES = kPiece * D;
+  static constexpr int STAGE = 2 * K_BYTES;
+  static constexpr int STAGES = 24576 / STAGE;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int OROW = D + 4;   // floats per row of the join, skewed over the banks
+  static constexpr int BARS = kWarps * RING;
+  static constexpr int ENTS = BARS + kWarps * STAGES * 8;
+  static constexpr int SMEM = ENTS + (kMaxEnt + 1) * 4 + 12;
+  static_assert(kWarps * 16 * (OROW + 2) * 4 <= kWarps * RING, "the join fits the rings");
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32"
+      " {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 0x80 in every byte that is an e4m3 NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// One query row's A operand halves: 16 dims at 64 c + 16 t of each 64-dim
+// part c, scaled by a power of two; returns the logit factor of the row.
+template <int D>
+__device__ __forceinline__ float load_query(const __nv_bfloat16* q, int t, bool valid, float scale_log2,
+                                            uint32_t (&h)[D / 64][8]) {
+  float x[D / 64][16];
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (valid) {
+      v[0] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t);
+      v[1] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t + 8);
+    }
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[c][2 * i] = __uint_as_float(w[i] << 16);
+      x[c][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      m = fmaxf(m, fmaxf(fabsf(x[c][2 * i]), fabsf(x[c][2 * i + 1])));
+    }
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  // largest element to [2^14, 2^15); rows of tiny or infinite elements are
+  // clamped so that both factors stay normal floats
+  const int e = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100), 127);
+  const float f = pow2(14 - e);
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[c][i] = half2_bits(x[c][2 * i] * f, x[c][2 * i + 1] * f);
+  return scale_log2 * pow2(e - 14);
+}
+
+// What a lane keeps of one upcoming piece of its warp.
+struct Piece {
+  int page;      // -1: outside the pool
+  int key0;      // position of its first key
+  int lo;        // first position that counts (0, or the window's)
+  float ks, lvs, ivs;
+};
+
+template <int D, bool SEL>
+__global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheCfg a) {
+  using C = CacheShape<D>;
+  constexpr int NT = D / 8;     // output column tiles
+  constexpr int VW = D / 32;    // words of a value row per lane
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * C::RING;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BARS) + warp * C::STAGES;
+  int32_t* ents = reinterpret_cast<int32_t*>(smem + C::ENTS);   // block | window flag in bit 30; then the count
+
+  const int split = blockIdx.x % a.splits;
+  const int unit = blockIdx.x / a.splits;
+  const int kvh = unit % a.h_kv;
+  const int tile = unit / a.h_kv % a.tiles;
+  const int seq = unit / a.h_kv / a.tiles;
+  const int len = min(max(__ldg(a.g.kv_len + seq), 0), a.max_pages * a.page);
+  // rows of the unit: row r is token (r0 + r) / G, head (r0 + r) % G
+  const int r0 = SEL ? tile * a.G : tile * 16;
+  const int n_rows = SEL ? a.G : min(16, a.n_q * a.G - r0);
+  const int first = len - a.n_q;                                // position of token 0
+  const int pos_lo = first + r0 / a.G, pos_hi = first + (r0 + n_rows - 1) / a.G;
+  const int pos_a = g < n_rows ? first + (r0 + g) / a.G : -1;   // rows g and g + 8 of this lane
+  const int pos_b = g + 8 < n_rows ? first + (r0 + g + 8) / a.G : -1;
+  const int ppb = a.page / kPiece;
+  const int32_t* table = a.g.table + static_cast<int64_t>(seq) * a.max_pages;
+  const int wlo = SEL ? max(pos_hi - a.window + 1, 0) : 0;
+
+  if (lane == 0)
+#pragma unroll
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[s], 1);
+  fence_barrier_init();
+  int n_pieces;
+  if (SEL) {
+    if (warp == 0) {
+      // the used selected blocks, then the window's blocks outside them
+      int n = 0;
+      if (pos_hi >= 0) {
+        const int32_t* row = a.g.idx + ((static_cast<int64_t>(seq) * a.n_q + tile) * a.h_kv + kvh) * a.topk;
+        const int nvis = (pos_hi + 1) / a.page;
+        const int v = lane < a.topk ? __ldg(row + lane) : -1;
+        const bool inrange = v >= 0 && v < nvis;
+        int run = inrange ? v : -1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+          if (lane >= o) run = max(run, y);
+        }
+        int prev = __shfl_up_sync(0xFFFFFFFFu, run, 1);
+        if (lane == 0) prev = -1;
+        const bool used = inrange && v > prev;
+        const uint32_t um = __ballot_sync(0xFFFFFFFFu, used);
+        if (used) ents[__popc(um & ((1u << lane) - 1))] = v;
+        n = __popc(um);
+        const int skipped = __popc(__ballot_sync(0xFFFFFFFFu, lane < a.topk && v != -1 && !used));
+        if (lane == 0 && split == 0 && skipped && a.g.bad) atomicAdd(a.g.bad, skipped);
+        __syncwarp();
+        const int w1 = pos_hi / a.page;
+        for (int b = wlo / a.page; b <= w1; b += 32) {
+          const int blk = b + lane;
+          bool add = blk <= w1;
+          for (int i = 0; i < __popc(um); ++i) add = add && ents[i] != blk;
+          const uint32_t am = __ballot_sync(0xFFFFFFFFu, add);
+          if (add) ents[n + __popc(am & ((1u << lane) - 1))] = blk | 1 << 30;
+          n += __popc(am);
+        }
+      }
+      if (lane == 0) ents[kMaxEnt] = n;
+    }
+    __syncthreads();
+    n_pieces = ents[kMaxEnt] * ppb;
+  } else {
+    __syncwarp();
+    n_pieces = pos_hi >= 0 ? pos_hi / kPiece + 1 : 0;
+  }
+  const int c0 = static_cast<int>(static_cast<int64_t>(n_pieces) * split / a.splits);
+  const int c1 = static_cast<int>(static_cast<int64_t>(n_pieces) * (split + 1) / a.splits);
+  const int n_my = max(0, (c1 - c0 - warp + kWarps - 1) / kWarps);
+
+  const auto fetch = [&](int i) {   // piece i of this warp, one per lane
+    Piece p;
+    p.page = -1;
+    p.key0 = p.lo = 0;
+    p.ks = p.lvs = p.ivs = 0.f;
+    if (i < n_my) {
+      const int c = c0 + warp + i * kWarps;
+      int blk = c / ppb;
+      if (SEL) {
+        const int e = ents[blk];
+        blk = e & ~(1 << 30);
+        p.lo = e >> 30 ? wlo : 0;
+      }
+      p.key0 = blk * a.page + (c % ppb) * kPiece;
+      const int page = __ldg(table + blk);
+      if (page >= 0 && page < a.n_pages) {
+        p.page = page;
+        const int64_t ph = static_cast<int64_t>(page) * a.h_kv + kvh;
+        p.ks = __ldg(a.g.ks + ph);
+        const float vs = fmaxf(__ldg(a.g.vs + ph), 1.17549435e-38f);
+        p.lvs = log2f(vs);
+        p.ivs = 1.f / vs;
+      } else if (a.g.bad) {
+        atomicAdd(a.g.bad, 1);
+      }
+    }
+    return p;
+  };
+  const auto issue = [&](int i, const Piece& from) {
+    const int page = __shfl_sync(0xFFFFFFFFu, from.page, i & 31);
+    const int key0 = __shfl_sync(0xFFFFFFFFu, from.key0, i & 31);
+    if (lane == 0) {
+      uint64_t* bar = &full[i % C::STAGES];
+      if (page < 0) {
+        mbar_arrive(bar);
+      } else {
+        uint8_t* dst = ring + (i % C::STAGES) * C::STAGE;
+        const int64_t off = ((static_cast<int64_t>(page) * a.h_kv + kvh) * a.page + key0 % a.page) * D;
+        mbar_arrive_expect_tx(bar, C::STAGE);
+        bulk_load(dst, a.g.kc + off, C::K_BYTES, bar);
+        bulk_load(dst + C::K_BYTES, a.g.vc + off, C::K_BYTES, bar);
+      }
+    }
+  };
+
+  Piece cur = fetch(lane), nxt = fetch(32 + lane);
+#pragma unroll
+  for (int i = 0; i < C::STAGES; ++i)
+    if (i < n_my) issue(i, cur);
+
+  // queries while the first copies fly
+  uint32_t qa[D / 64][8], qb[D / 64][8];
+  float fa, fb;
+  {
+    const auto row = [&](int r) {
+      const int R = r0 + r, i = R / a.G, h = R % a.G;
+      return static_cast<const __nv_bfloat16*>(a.g.Q) +
+             ((static_cast<int64_t>(seq) * a.n_q + i) * a.h_q + kvh * a.G + h) * D;
+    };
+    fa = load_query<D>(row(g < n_rows ? g : 0), t, g < n_rows, a.scale_log2, qa);
+    fb = load_query<D>(row(g + 8 < n_rows ? g + 8 : 0), t, g + 8 < n_rows, a.scale_log2, qb);
+  }
+
+  float O[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) O[j][c] = 0.f;
+  float Ma = -INFINITY, Mb = -INFINITY, la = 0.f, lb = 0.f;
+
+  int done = 0;
+  for (; done < n_my; ++done) {
+    const int i = done, b = i & 31;
+    if (b == 0 && i > 0) {
+      cur = nxt;
+      nxt = fetch(i + 32 + lane);
+    }
+    const int page = __shfl_sync(0xFFFFFFFFu, cur.page, b);
+    const int key0 = __shfl_sync(0xFFFFFFFFu, cur.key0, b);
+    const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, b);
+    const float lvs = __shfl_sync(0xFFFFFFFFu, cur.lvs, b);
+    const float ivs = __shfl_sync(0xFFFFFFFFu, cur.ivs, b);
+    const int lo = SEL ? __shfl_sync(0xFFFFFFFFu, cur.lo, b) : 0;
+    const int st = i % C::STAGES;
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::STAGES) & 1, a.err, SITE_CACHE_FULL))) break;
+    if (page >= 0) {
+      const uint8_t* sK = ring + st * C::STAGE;
+      const uint8_t* sV = sK + C::K_BYTES;
+      const bool partial = key0 + kPiece - 1 > pos_lo || key0 < lo;
+      // S = Q K^T: key tile nt holds keys nt*8 .. nt*8+7, this lane's key nt*8+g
+      float S[4][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[nt][c] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 kv = *reinterpret_cast<const uint4*>(sK + (nt * 8 + g) * D + c * 64 + t * 16);
+          const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t A[4] = {qa[c][2 * s], qb[c][2 * s], qa[c][2 * s + 1], qb[c][2 * s + 1]};
+            mma_f16(S[nt], A, e4m3x2_to_half2(w[s] & 0xFFFFu), e4m3x2_to_half2(w[s] >> 16));
+          }
+        }
+      }
+      const float ka = fa * ks, kb = fb * ks;
+      float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          S[nt][c] = fmaf(S[nt][c], ka, lvs);
+          S[nt][2 + c] = fmaf(S[nt][2 + c], kb, lvs);
+          if (partial) {
+            const int kp = key0 + nt * 8 + 2 * t + c;
+            if (kp > pos_a || kp < lo) S[nt][c] = -INFINITY;
+            if (kp > pos_b || kp < lo) S[nt][2 + c] = -INFINITY;
+          }
+          ma = fmaxf(ma, S[nt][c]);
+          mb = fmaxf(mb, S[nt][2 + c]);
+        }
+      }
+      ma = fmaxf(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 1));
+      mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 1));
+      ma = fmaxf(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 2));
+      mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 2));
+      if (__any_sync(0xFFFFFFFFu, ma > Ma || mb > Mb)) {   // a maximum moved: rescale
+        const float na = fmaxf(Ma, ma), nb = fmaxf(Mb, mb);
+        const float xa = na == -INFINITY ? 1.f : fast_exp2(Ma - na), xb = nb == -INFINITY ? 1.f : fast_exp2(Mb - nb);
+        Ma = na;
+        Mb = nb;
+        la *= xa;
+        lb *= xb;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          O[j][0] *= xa;
+          O[j][1] *= xa;
+          O[j][2] *= xb;
+          O[j][3] *= xb;
+        }
+      }
+      const float ra = Ma == -INFINITY ? 0.f : Ma, rb = Mb == -INFINITY ? 0.f : Mb;
+      float sa = 0.f, sb = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          S[nt][c] = fast_exp2(S[nt][c] - ra);
+          S[nt][2 + c] = fast_exp2(S[nt][2 + c] - rb);
+          sa += S[nt][c];
+          sb += S[nt][2 + c];
+        }
+      }
+      la = fmaf(sa, ivs, la);
+      lb = fmaf(sb, ivs, lb);
+      // O += P V: keys 16 q + {2t, 2t+1, 2t+8, 2t+9}, this lane's output
+      // columns NT g + j
+      uint32_t odd = 0;   // NaN among values that not every row attends
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t A[4] = {half2_bits(S[2 * q][0], S[2 * q][1]), half2_bits(S[2 * q][2], S[2 * q][3]),
+                               half2_bits(S[2 * q + 1][0], S[2 * q + 1][1]),
+                               half2_bits(S[2 * q + 1][2], S[2 * q + 1][3])};
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 16 * q + 2 * t + (k & 1) + 8 * (k >> 1);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sV + key * D + g * 16);
+            v[k][0] = x.x; v[k][1] = x.y; v[k][VW - 2] = x.z; v[k][VW - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(sV + key * D + g * 8);
+            v[k][0] = x.x; v[k][1] = x.y;
+          }
+          if (partial) {
+            const int kp = key0 + key;
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              if (kp > pos_hi || kp < lo) {
+                v[k][w] = 0;   // no row attends it
+              } else {
+                const uint32_t n = nan_bytes(v[k][w]);
+                odd |= n;
+                v[k][w] &= ~((n >> 7) * 0xFFu);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t e0 = __byte_perm(v[0][w], v[1][w], 0x5140), e1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t o0 = __byte_perm(v[2][w], v[3][w], 0x5140), o1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          mma_f16(O[4 * w + 0], A, e4m3x2_to_half2(e0 & 0xFFFFu), e4m3x2_to_half2(o0 & 0xFFFFu));
+          mma_f16(O[4 * w + 1], A, e4m3x2_to_half2(e0 >> 16), e4m3x2_to_half2(o0 >> 16));
+          mma_f16(O[4 * w + 2], A, e4m3x2_to_half2(e1 & 0xFFFFu), e4m3x2_to_half2(o1 & 0xFFFFu));
+          mma_f16(O[4 * w + 3], A, e4m3x2_to_half2(e1 >> 16), e4m3x2_to_half2(o1 >> 16));
+        }
+      }
+      if (partial && __any_sync(0xFFFFFFFFu, odd != 0)) {
+        // 0 * NaN is NaN: such values stay out of the product and reach the
+        // rows that attend them here
+        const float bad = __int_as_float(0x7FFFFFFF);
+        for (int key = 0; key < kPiece; ++key) {
+          const int kp = key0 + key;
+          if (kp > pos_hi || kp < lo) continue;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if ((sV[key * D + (2 * t + c) * NT + j] & 0x7F) == 0x7F) {
+                if (kp <= pos_a) O[j][c] = bad;
+                if (kp <= pos_b) O[j][2 + c] = bad;
+              }
+        }
+      }
+    }
+    __syncwarp();   // every lane has read the stage
+    const int ahead = i + C::STAGES;
+    if (ahead < n_my) {
+      const bool same = ahead / 32 == i / 32;
+      Piece from;
+      from.page = same ? cur.page : nxt.page;
+      from.key0 = same ? cur.key0 : nxt.key0;
+      issue(ahead, from);
+    }
+  }
+  if (done < n_my) {   // a wait gave up: let the copies in flight land
+    const uint64_t t0 = global_timer_ns();
+    for (int i = done; i < min(done + C::STAGES, n_my); ++i)
+      while (!mbar_try_wait(&full[i % C::STAGES], (i / C::STAGES) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  }
+
+  // join the four warps: maxima and sums, then outputs, through the rings
+  la += __shfl_xor_sync(0xFFFFFFFFu, la, 1);
+  lb += __shfl_xor_sync(0xFFFFFFFFu, lb, 1);
+  la += __shfl_xor_sync(0xFFFFFFFFu, la, 2);
+  lb += __shfl_xor_sync(0xFFFFFFFFu, lb, 2);
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(smem);                                     // [warps][16][OROW]
+  float2* jml = reinterpret_cast<float2*>(jo + kWarps * 16 * C::OROW);            // [warps][16]
+  if (t == 0) {
+    jml[warp * 16 + g] = make_float2(Ma, la);
+    jml[warp * 16 + g + 8] = make_float2(Mb, lb);
+  }
+  {
+    float* ra = jo + (warp * 16 + g) * C::OROW + 2 * t * NT;
+    float* rb = ra + 8 * C::OROW;
+    const bool wa = g < n_rows, wb = g + 8 < n_rows;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < NT; j += 4) {
+        if (wa) *reinterpret_cast<float4*>(ra + c * NT + j) = make_float4(O[j][c], O[j + 1][c], O[j + 2][c], O[j + 3][c]);
+        if (wb)
+          *reinterpret_cast<float4*>(rb + c * NT + j) =
+              make_float4(O[j][2 + c], O[j + 1][2 + c], O[j + 2][2 + c], O[j + 3][2 + c]);
+      }
+  }
+  __syncthreads();
+  constexpr int QR = D / 4;   // threads per row
+  for (int x = threadIdx.x; x < n_rows * QR; x += kWarps * 32) {
+    const int r = x / QR, q = x % QR;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, jml[w * 16 + r].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = jml[w * 16 + r];
+      const float f = M == -INFINITY ? 1.f : exp2f(ml.x - M);
+      const float4 y = *reinterpret_cast<const float4*>(jo + (w * 16 + r) * C::OROW + 4 * q);
+      l = fmaf(f, ml.y, l);
+      o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
+    }
+    if (a.splits > 1) {
+      const int64_t pr = (static_cast<int64_t>(unit) * a.splits + split) * a.rows + r;
+      reinterpret_cast<float4*>(a.part_o + pr * D)[q] = o;
+      if (q == 0) a.part_ml[pr] = make_float2(M, l);
+    } else {
+      const int R = r0 + r;
+      const int64_t row = (static_cast<int64_t>(seq) * a.n_q + R / a.G) * a.h_q + kvh * a.G + R % a.G;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint2 out;
+      out.x = pack_bf16(o.x * inv, o.y * inv);
+      out.y = pack_bf16(o.z * inv, o.w * inv);
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.g.O) + row * D)[q] = out;
+      if (q == 0 && a.g.lse) a.g.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// Joins the splits of every row: one warp per row.
+template <int D, bool SEL>
+__global__ void __launch_bounds__(128) cache_join_kernel(const CacheCfg a) {
+  constexpr int E = D / 32;   // dims per lane
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+  const int64_t unit = item / a.rows;
+  const int r = static_cast<int>(item % a.rows);
+  if (unit >= static_cast<int64_t>(a.n_seq) * a.tiles * a.h_kv) return;
+  const int kvh = static_cast<int>(unit % a.h_kv);
+  const int tile = static_cast<int>(unit / a.h_kv % a.tiles);
+  const int seq = static_cast<int>(unit / a.h_kv / a.tiles);
+  const int R = (SEL ? tile * a.G : tile * 16) + r;
+  if (R >= a.n_q * a.G) return;
+  const float2* ml = a.part_ml + unit * a.splits * a.rows + r;
+  const float* po = a.part_o + (unit * a.splits * a.rows + r) * D + lane * E;
+  float M = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, ml[static_cast<int64_t>(s) * a.rows].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[static_cast<int64_t>(s) * a.rows];
+    const float f = M == -INFINITY ? 1.f : exp2f(x.x - M);
+    const float* y = po + static_cast<int64_t>(s) * a.rows * D;
+    l = fmaf(f, x.y, l);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(y + e);
+      acc[e] = fmaf(f, v.x, acc[e]);
+      acc[e + 1] = fmaf(f, v.y, acc[e + 1]);
+    }
+  }
+  const int64_t row = (static_cast<int64_t>(seq) * a.n_q + R / a.G) * a.h_q + kvh * a.G + R % a.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.g.O) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && a.g.lse) a.g.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+struct Split {
+  int64_t units;
+  int tiles, rows, splits;
+};
+
+Split split_of(const ssa_cache_attn_params& p) {
+  Split s;
+  const int G = p.h_q / p.h_kv;
+  const bool sel = p.topk > 0;
+  s.tiles = sel ? p.n_q : (p.n_q * G + 15) / 16;
+  s.rows = sel ? G : (p.n_q * G < 16 ? p.n_q * G : 16);
+  s.units = static_cast<int64_t>(p.n_seq) * p.h_kv * s.tiles;
+  int64_t pieces = static_cast<int64_t>(p.max_pages) * p.page / kPiece;
+  if (sel) {
+    const int64_t most = (p.topk + p.window / p.page + 2) * static_cast<int64_t>(p.page / kPiece);
+    if (pieces > most) pieces = most;
+  }
+  // two blocks per SM run at a time: one wave of them when the units are
+  // fewer, else about three, so that ragged lengths even out; at least four
+  // pieces per warp
+  const int64_t room = 2 * kSmCount;
+  int64_t n = s.units < 1 ? 1 : s.units < room ? room / s.units : (3 * room + s.units - 1) / s.units;
+  if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
+  s.splits = static_cast<int>(n < 1 ? 1 : n);
+  return s;
+}
+
+template <int D, bool SEL>
+cudaError_t run_cache_attn(const CacheCfg& a, int64_t units, const LaunchCtx& c) {
+  using C = CacheShape<D>;
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  if (units * a.splits > INT32_MAX) return cudaErrorInvalidValue;
+  cache_attn_kernel<D, SEL><<<static_cast<unsigned>(units * a.splits), kWarps * 32, C::SMEM, c.stream>>>(a);
+  note_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+  cache_join_kernel<D, SEL><<<static_cast<unsigned>((units * a.rows + 3) / 4), 128, 0, c.stream>>>(a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_attn_ws(const ssa_cache_attn_params& p) {
+  const Split s = split_of(p);
+  if (s.splits == 1) return 0;
+  return static_cast<size_t>(s.units) * s.splits * s.rows * (p.d * 4 + 8);
+}
+
+cudaError_t launch_cache_attn(const ssa_cache_attn_params& p, const CacheAttnArgs& g, const LaunchCtx& c) {
+  const Split s = split_of(p);
+  CacheCfg a{};
+  a.g = g;
+  a.n_seq = p.n_seq; a.n_q = p.n_q; a.max_pages = p.max_pages; a.n_pages = p.n_pages; a.page = p.page;
+  a.h_q = p.h_q; a.h_kv = p.h_kv; a.G = p.h_q / p.h_kv; a.topk = p.topk; a.window = p.window;
+  a.tiles = s.tiles; a.rows = s.rows; a.splits = s.splits;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.part_o = static_cast<float*>(g.ws);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(s.units) * s.splits * s.rows * p.d);
+  a.err = c.err;
+  if (p.d == 128)
+    return p.topk ? run_cache_attn<128, true>(a, s.units, c) : run_cache_attn<128, false>(a, s.units, c);
+  return p.topk ? run_cache_attn<64, true>(a, s.units, c) : run_cache_attn<64, false>(a, s.units, c);
+}
+
+}  // namespace ssa

@@ -21,6 +21,14 @@ struct LaunchCtx {
 // Counts every kernel launched through the library.
 void note_launch();
 
+// The current device's launch context (SSA_ERR_CUDA when there is none).
+ssa_status make_launch_ctx(void* stream, LaunchCtx& c);
+
+// 3D bf16 map of a [rows, heads, d] operand with `stride` elements between
+// rows; 128-byte-swizzled boxes of 64 dims x box_heads heads x box_rows rows.
+bool encode_heads(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, int64_t stride, int box_heads,
+                  int box_rows);
+
 // step (i): block summaries
 cudaError_t launch_summary(const ssa_params& p, const void* K, float* mu, float* sigma,
                            void* table, const LaunchCtx& c);
@@ -199,6 +207,33 @@ struct HierProbeArgs {
   const float* sbound;         // [bgs]
 };
 cudaError_t launch_hier_probe(const ssa_params& p, const HierProbeArgs& a, const LaunchCtx& c);
+
+// Serving operators (serve_api.cu).
+cudaError_t launch_qk_rope(const ssa_rope_params& p, const void* Q, const void* K, const float* qw, const float* kw,
+                           const double* freq, const int32_t* positions, void* Qo, void* Ko, const LaunchCtx& c);
+struct AppendArgs {
+  const void *K, *V;
+  const float* k_weight;
+  const double* freq;
+  const int32_t *new_start, *cached, *table;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  int32_t* bad;
+};
+cudaError_t launch_cache_append(const ssa_append_params& p, const AppendArgs& a, const LaunchCtx& c);
+struct CacheAttnArgs {
+  const void* Q;
+  const int32_t *table, *kv_len;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  const int32_t* idx;
+  void* O;
+  float* lse;
+  int32_t* bad;
+  void* ws;
+};
+size_t cache_attn_ws(const ssa_cache_attn_params& p);
+cudaError_t launch_cache_attn(const ssa_cache_attn_params& p, const CacheAttnArgs& a, const LaunchCtx& c);
 
 // One CTA whose bounded wait never completes (the failure-path self-test).
 cudaError_t launch_selftest_wait(const LaunchCtx& c);

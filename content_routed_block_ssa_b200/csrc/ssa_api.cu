@@ -637,6 +637,22 @@ ssa_status do_route_hier(const ssa_params& p, const ssa_hier_params& hp, const v
 
 namespace ssa {
 size_t route_min_workspace(const ssa_params& p) { return check_params(&p) == SSA_OK ? features_bytes(p) : 0; }
+
+ssa_status make_launch_ctx(void* stream, LaunchCtx& c) { return make_ctx(stream, c); }
+
+bool encode_heads(CUtensorMap* m, const void* base, int d, int heads, int64_t rows, int64_t stride, int box_heads,
+                  int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace ssa
 
 extern "C" {

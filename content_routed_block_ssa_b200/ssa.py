@@ -20,6 +20,8 @@ SSA_OK, SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED, SSA_ERR_WORKSPACE, SSA_ERR_CUD
 SSA_F32, SSA_BF16 = 0, 1
 SSA_SIGMA_DIAG, SSA_SIGMA_FULL = 0, 1
 SSA_ROUTE_AUTO, SSA_ROUTE_TILED, SSA_ROUTE_ROWWISE = 0, 1, 2
+SSA_ROPE_HALF, SSA_ROPE_PAIRS = 0, 1
+SSA_ROPE_PLAIN, SSA_ROPE_LINEAR, SSA_ROPE_BASE, SSA_ROPE_BLEND = 0, 1, 2, 3
 
 
 class SSAError(RuntimeError):
@@ -44,6 +46,35 @@ class ssa_hier_params(C.Structure):
 
 
 assert C.sizeof(ssa_hier_params) == 16
+
+
+class ssa_rope_params(C.Structure):
+    _fields_ = [("n_tokens", C.c_int32), ("h_q", C.c_int32), ("h_kv", C.c_int32), ("d", C.c_int32),
+                ("rot", C.c_int32), ("layout", C.c_int32), ("dtype", C.c_int32), ("norm", C.c_int32),
+                ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("q_out_stride", C.c_int64),
+                ("k_out_stride", C.c_int64), ("eps", C.c_float), ("mscale", C.c_float)]
+
+
+assert C.sizeof(ssa_rope_params) == 72
+
+
+class ssa_append_params(C.Structure):
+    _fields_ = [("n_tokens", C.c_int32), ("n_seq", C.c_int32), ("max_pages", C.c_int32), ("n_pages", C.c_int32),
+                ("page", C.c_int32), ("h_kv", C.c_int32), ("d", C.c_int32), ("rot", C.c_int32),
+                ("layout", C.c_int32), ("dtype", C.c_int32), ("norm", C.c_int32), ("reserved", C.c_int32),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("eps", C.c_float), ("mscale", C.c_float)]
+
+
+assert C.sizeof(ssa_append_params) == 72
+
+
+class ssa_cache_attn_params(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("n_q", C.c_int32), ("max_pages", C.c_int32), ("n_pages", C.c_int32),
+                ("page", C.c_int32), ("h_q", C.c_int32), ("h_kv", C.c_int32), ("d", C.c_int32),
+                ("topk", C.c_int32), ("window", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
+assert C.sizeof(ssa_cache_attn_params) == 48
 
 
 def _load():
@@ -77,6 +108,12 @@ def _load():
         "ssa_hier_nodes": (i32, [P, H, vp, vp, vp]),
         "ssa_route_hier_workspace_size": (sz, [P, H]),
         "ssa_route_hier": (i32, [P, H, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "ssa_rope_frequencies": (i32, [i32, i32, C.c_double, C.c_double, C.c_double, C.c_double, C.c_double, vp,
+                                       C.POINTER(C.c_float)]),
+        "ssa_qk_rope": (i32, [C.POINTER(ssa_rope_params)] + [vp] * 9),
+        "ssa_cache_append": (i32, [C.POINTER(ssa_append_params)] + [vp] * 13),
+        "ssa_cache_attn_workspace_size": (sz, [C.POINTER(ssa_cache_attn_params)]),
+        "ssa_cache_attn": (i32, [C.POINTER(ssa_cache_attn_params)] + [vp] * 12 + [sz, vp]),
         "ssa_selftest_wait_timeout": (i32, [vp]),
     }
     for name, (res, args) in sig.items():
@@ -94,6 +131,8 @@ EXPORTED = ("ssa_status_string", "ssa_version", "ssa_launch_count", "ssa_device_
             "ssa_attn_window", "ssa_attn_merge",
             "ssa_workspace_size", "ssa_forward", "ssa_hostio_buffer_size", "ssa_forward_hostio",
             "ssa_hier_nodes_size", "ssa_hier_nodes", "ssa_route_hier_workspace_size", "ssa_route_hier",
+            "ssa_rope_frequencies", "ssa_qk_rope", "ssa_cache_append", "ssa_cache_attn_workspace_size",
+            "ssa_cache_attn",
             "ssa_selftest_wait_timeout")
 
 
@@ -313,6 +352,133 @@ def hier_super_views(p, hp, nodes):
     rad = nodes[r_off:r_off + bgs * ns * 4].view(torch.float32).view(p.batch, p.h_kv, ns)
     bnd = nodes[b_off:b_off + bgs * 4].view(torch.float32).view(p.batch, p.h_kv)
     return rows, rad, bnd
+
+
+# ---------------------------------------------------------------- serving operators
+
+_ROPE_LAYOUT = {"half": SSA_ROPE_HALF, "pairs": SSA_ROPE_PAIRS}
+_ROPE_SCHEDULE = {"plain": SSA_ROPE_PLAIN, "linear": SSA_ROPE_LINEAR, "base": SSA_ROPE_BASE, "blend": SSA_ROPE_BLEND}
+_DTYPE = {"f32": SSA_F32, "bf16": SSA_BF16}
+_TORCH = {SSA_F32: torch.float32, SSA_BF16: torch.bfloat16}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def rope_frequencies(rot, base=10000.0, schedule="plain", factor=1.0, trained_len=0.0, fast=32.0, slow=1.0):
+    """(angles per position [rot/2] float64 on the host, mscale) of a schedule:
+    'plain', 'linear' (positions interpolated), 'base' (a larger base) or
+    'blend' (YaRN).  Copy the table to the device once and keep it."""
+    freq = torch.zeros(max(int(rot) // 2, 1), dtype=torch.float64)
+    m = C.c_float(1.0)
+    _check(lib.ssa_rope_frequencies(_ROPE_SCHEDULE.get(schedule, schedule), rot, base, factor, trained_len, fast, slow,
+                                    freq.data_ptr(), C.byref(m)), "ssa_rope_frequencies")
+    return freq, float(m.value)
+
+
+def make_rope_params(n_tokens, h_q, h_kv, d, rot=None, layout="half", dtype="bf16", norm=True, eps=1e-6, mscale=1.0,
+                     q_stride=None, k_stride=None, q_out_stride=None, k_out_stride=None) -> ssa_rope_params:
+    """An ssa_rope_params struct (rot None: the whole head; strides None: dense)."""
+    return ssa_rope_params(n_tokens=n_tokens, h_q=h_q, h_kv=h_kv, d=d, rot=d if rot is None else rot,
+                           layout=_ROPE_LAYOUT.get(layout, layout), dtype=_DTYPE.get(dtype, dtype),
+                           norm=1 if norm else 0, q_stride=h_q * d if q_stride is None else q_stride,
+                           k_stride=h_kv * d if k_stride is None else k_stride,
+                           q_out_stride=h_q * d if q_out_stride is None else q_out_stride,
+                           k_out_stride=h_kv * d if k_out_stride is None else k_out_stride, eps=eps, mscale=mscale)
+
+
+def make_append_params(n_tokens, n_seq, max_pages, n_pages, page, h_kv, d, rot=None, layout="half", dtype="bf16",
+                       norm=True, eps=1e-6, mscale=1.0, k_stride=None, v_stride=None) -> ssa_append_params:
+    """An ssa_append_params struct (rot None: the whole head; strides None: dense)."""
+    return ssa_append_params(n_tokens=n_tokens, n_seq=n_seq, max_pages=max_pages, n_pages=n_pages, page=page,
+                             h_kv=h_kv, d=d, rot=d if rot is None else rot, layout=_ROPE_LAYOUT.get(layout, layout),
+                             dtype=_DTYPE.get(dtype, dtype), norm=1 if norm else 0,
+                             k_stride=h_kv * d if k_stride is None else k_stride,
+                             v_stride=h_kv * d if v_stride is None else v_stride, eps=eps, mscale=mscale)
+
+
+def make_cache_attn_params(n_seq, n_q, max_pages, n_pages, page, h_q, h_kv, d, topk=0, window=0,
+                           scale=None) -> ssa_cache_attn_params:
+    """An ssa_cache_attn_params struct (topk 0: every key; scale None: 1/sqrt(d))."""
+    return ssa_cache_attn_params(n_seq=n_seq, n_q=n_q, max_pages=max_pages, n_pages=n_pages, page=page, h_q=h_q,
+                                 h_kv=h_kv, d=d, topk=topk, window=window,
+                                 scale=(1.0 / math.sqrt(d)) if scale is None else scale)
+
+
+def _arg(name, t, shape, dtype, stride=None):
+    """Address of an operand of a serving operator, after its checks: type,
+    shape, layout (dense, or with `stride` the heads dense within a token and
+    that many elements between tokens) and the current device."""
+    if t is None:
+        return None
+    if (t.dtype not in dtype) if isinstance(dtype, tuple) else (t.dtype is not dtype):
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.numel():
+        if stride is None:
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: libssa needs a dense row-major buffer here; got strides {t.stride()}")
+        else:
+            s = t.stride()
+            if s[2] != 1 or (s[1] != shape[2] and shape[1] > 1) or (s[0] != stride and shape[0] > 1):
+                raise ValueError(f"{name}: expected strides ({stride}, {shape[2]}, 1), got {s}")
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: expected a tensor on the current CUDA device, got one on {t.device}")
+    return t.data_ptr()
+
+
+def ssa_qk_rope(p, Q, K, q_weight, k_weight, freq, positions, Q_out, K_out, stream=None):
+    """Norms of queries and keys per head and their position rotation."""
+    dt = _TORCH.get(p.dtype)
+    q, k, w = (p.n_tokens, p.h_q, p.d), (p.n_tokens, p.h_kv, p.d), (p.d,)
+    _check(lib.ssa_qk_rope(C.byref(p), _arg("Q", Q, q, dt, p.q_stride), _arg("K", K, k, dt, p.k_stride),
+                           _arg("q_weight", q_weight, w, torch.float32), _arg("k_weight", k_weight, w, torch.float32),
+                           _arg("freq", freq, (p.rot // 2,), torch.float64),
+                           _arg("positions", positions, (p.n_tokens,), torch.int32),
+                           _arg("Q_out", Q_out, q, dt, p.q_out_stride), _arg("K_out", K_out, k, dt, p.k_out_stride),
+                           _stream(stream)), "ssa_qk_rope")
+
+
+def cache_shapes(p):
+    """Shapes of the paged cache's codes (uint8) and scales (float32), of K and V each."""
+    return (p.n_pages, p.h_kv, p.page, p.d), (p.n_pages, p.h_kv)
+
+
+def _cache_args(p, k_cache, v_cache, k_scale, v_scale):
+    codes, scales = cache_shapes(p)
+    return (_arg("k_cache", k_cache, codes, _CODES), _arg("v_cache", v_cache, codes, _CODES),
+            _arg("k_scale", k_scale, scales, torch.float32), _arg("v_scale", v_scale, scales, torch.float32))
+
+
+def ssa_cache_append(p, K, V, k_weight, freq, new_start, cached, page_table, k_cache, v_cache, k_scale, v_scale,
+                     bad_count=None, stream=None):
+    """Appends keys (normed, rotated) and values to the paged 8-bit cache."""
+    dt, kv = _TORCH.get(p.dtype), (p.n_tokens, p.h_kv, p.d)
+    _check(lib.ssa_cache_append(C.byref(p), _arg("K", K, kv, dt, p.k_stride), _arg("V", V, kv, dt, p.v_stride),
+                                _arg("k_weight", k_weight, (p.d,), torch.float32),
+                                _arg("freq", freq, (p.rot // 2,), torch.float64),
+                                _arg("new_start", new_start, (p.n_seq + 1,), torch.int32),
+                                _arg("cached", cached, (p.n_seq,), torch.int32),
+                                _arg("page_table", page_table, (p.n_seq, p.max_pages), torch.int32),
+                                *_cache_args(p, k_cache, v_cache, k_scale, v_scale),
+                                _arg("bad_count", bad_count, (1,), torch.int32), _stream(stream)), "ssa_cache_append")
+
+
+def ssa_cache_attn_workspace_size(p) -> int:
+    return int(lib.ssa_cache_attn_workspace_size(C.byref(p)))
+
+
+def ssa_cache_attn(p, Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale, block_idx, O, lse=None,
+                   bad_count=None, ws=None, stream=None):
+    """Attention of new tokens over the paged 8-bit cache."""
+    q = (p.n_seq, p.n_q, p.h_q, p.d)
+    _check(lib.ssa_cache_attn(C.byref(p), _arg("Q", Q, q, torch.bfloat16),
+                              _arg("page_table", page_table, (p.n_seq, p.max_pages), torch.int32),
+                              _arg("kv_len", kv_len, (p.n_seq,), torch.int32),
+                              *_cache_args(p, k_cache, v_cache, k_scale, v_scale),
+                              _arg("block_idx", block_idx, (p.n_seq, p.n_q, p.h_kv, p.topk), torch.int32),
+                              _arg("O", O, q, torch.bfloat16), _arg("lse", lse, q[:3], torch.float32),
+                              _arg("bad_count", bad_count, (1,), torch.int32), _ptr(ws), _nbytes(ws),
+                              _stream(stream)), "ssa_cache_attn")
 
 
 SITE_SELFTEST = 0x7F1

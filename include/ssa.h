@@ -418,6 +418,194 @@ SSA_API ssa_status ssa_route_hier(const ssa_params* p, const ssa_hier_params* hp
                                   uint8_t* certified, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Serving operators around the layer
+ * ==================================
+ * What a serving program does with queries, keys and values before and
+ * beside the layer: the norm and position rotation of queries and keys, a
+ * paged 8-bit cache of keys and values, attention over that cache for new
+ * tokens (all keys, or the blocks ssa_route_topk selected plus the window),
+ * and causal attention over packed prompts of different lengths.  The
+ * conventions above hold (caller-owned device buffers, 16-byte aligned,
+ * arguments checked before any launch, asynchronous on `stream`, launched on
+ * the current device).  Tokens of an operand marked "strided" may lie further
+ * apart than their heads take: token t, head h starts at element
+ * t * stride + h * d, so that the heads of a joint q/k/v projection are used
+ * where they are; a stride is at least heads * d elements and a multiple of
+ * 16 bytes.
+ *
+ * Lengths, offsets, page numbers and positions are read on the GPU.  Values
+ * that do not fit (a page outside the pool, a length beyond the page table, a
+ * decreasing offset) never address memory: the tokens or keys that they name
+ * are left out and, where the call has a bad_count, counted into it
+ * (atomically added, not reset).
+ */
+
+/* Pairing of the rotated dims: (i, i + rot/2), or (2i, 2i + 1). */
+typedef enum { SSA_ROPE_HALF = 0, SSA_ROPE_PAIRS = 1 } ssa_rope_layout;
+/* Frequency schedules of ssa_rope_frequencies. */
+typedef enum {
+  SSA_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot)                                  */
+  SSA_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated)                 */
+  SSA_ROPE_BASE = 2,   /* base * factor^(rot/(rot-2)) in place of base          */
+  SSA_ROPE_BLEND = 3   /* YaRN: f_i / factor for pairs that turn less than slow
+                          times over trained_len positions, f_i for those that
+                          turn more than fast times, a linear blend between    */
+} ssa_rope_schedule;
+
+/*
+ * Host function: the rot/2 angles per position (radians, float64) of a
+ * schedule into the HOST array freq, and into *mscale (may be NULL) the
+ * factor on the rotated dims that the schedule asks for: 0.1 ln(factor) + 1
+ * for SSA_ROPE_BLEND with factor > 1, else 1.  The blend runs over the pair
+ * indexes between floor(x(fast)) and ceil(x(slow)), clamped to [0, rot-1],
+ * x(t) = rot ln(trained_len / (2 pi t)) / (2 ln base) (the YaRN paper,
+ * section 3.2).  rot even, >= 2; base > 1; factor >= 1; and, for the blend,
+ * trained_len >= 1 and fast > slow > 0, else SSA_ERR_INVALID_ARG.  Any other
+ * table of finite frequencies may be given to the kernels instead.
+ */
+SSA_API ssa_status ssa_rope_frequencies(int32_t schedule, int32_t rot, double base, double factor,
+                                        double trained_len, double fast, double slow, double* freq,
+                                        float* mscale);
+
+/* 72 bytes, no padding. */
+typedef struct {
+  int32_t n_tokens;
+  int32_t h_q, h_kv;  /* heads of q and of k (any counts >= 1)                  */
+  int32_t d;          /* 64 or 128                                              */
+  int32_t rot;        /* rotated dims: a multiple of 16 in 0..d (0: none)       */
+  int32_t layout;     /* ssa_rope_layout                                        */
+  int32_t dtype;      /* ssa_dtype of Q, K and the outputs                      */
+  int32_t norm;       /* 1: divide each head by its root mean square; 0: not    */
+  int64_t q_stride, k_stride;         /* elements between tokens of Q, K        */
+  int64_t q_out_stride, k_out_stride; /* ... of the outputs                     */
+  float eps;          /* added to the mean square; finite, >= 0                 */
+  float mscale;       /* factor on the rotated dims; finite                     */
+} ssa_rope_params;
+
+/*
+ * Norms of queries and keys per head and their position rotation, in one
+ * pass: y = x / sqrt(mean(x^2) + eps) * weight over the d dims of each head
+ * (norm = 1), then every pair (a, b) of the first rot dims turns by
+ * angle = position * freq[i]: (a, b) -> mscale (a cos - b sin, b cos + a sin).
+ * Computed in float32 and rounded once.  Angles are reduced to one turn in
+ * 64-bit fixed point, so far positions lose nothing; positions may be
+ * negative.
+ *   Q, K          strided device [n_tokens, h_q | h_kv, d] of dtype
+ *   q_weight, k_weight  device float32 [d], may be NULL (ones); norm = 0
+ *                 ignores them
+ *   freq          device float64 [rot/2] (may be NULL when rot = 0)
+ *   positions     device int32 [n_tokens] (may be NULL when rot = 0)
+ *   Q_out, K_out  strided device outputs; each may be its own input (same
+ *                 address and stride) and otherwise overlaps no operand
+ */
+SSA_API ssa_status ssa_qk_rope(const ssa_rope_params* p, const void* Q, const void* K, const float* q_weight,
+                               const float* k_weight, const double* freq, const int32_t* positions,
+                               void* Q_out, void* K_out, void* stream);
+
+/*
+ * The paged 8-bit cache.  A pool of n_pages pages holds `page` tokens each
+ * (64 or 128: the layer's routing block), for every kv-head:
+ *   k_cache, v_cache  device uint8 [n_pages, h_kv, page, d], e4m3 codes
+ *   k_scale, v_scale  device float32 [n_pages, h_kv], powers of two: a value
+ *                     is its code times the scale of its page and kv-head
+ *   page_table        device int32 [n_seq, max_pages]: token j of sequence s
+ *                     lies in slot j % page of page page_table[s][j / page];
+ *                     entries behind a sequence's last page are not read
+ * A page may stand in several sequences' rows (a shared prefix) as long as
+ * no call appends to it through more than one of them.
+ */
+
+/* 72 bytes, no padding. */
+typedef struct {
+  int32_t n_tokens;   /* rows of K and V                                        */
+  int32_t n_seq;
+  int32_t max_pages;  /* row length of page_table                               */
+  int32_t n_pages;    /* pages in the pool                                      */
+  int32_t page;       /* tokens per page: 64 or 128                             */
+  int32_t h_kv, d;    /* d 64 or 128                                            */
+  int32_t rot;        /* rotated dims of the keys, as in ssa_rope_params        */
+  int32_t layout, dtype, norm;
+  int32_t reserved;   /* 0                                                      */
+  int64_t k_stride, v_stride;
+  float eps, mscale;
+} ssa_append_params;
+
+/*
+ * Appends new tokens to the cache.  Sequence s gets tokens new_start[s] ..
+ * new_start[s+1] - 1 of K and V at positions cached[s], cached[s] + 1, ...;
+ * keys are normed and rotated on the way as by ssa_qk_rope (the rotation's
+ * position is the token's place in its sequence), values are stored as they
+ * are.  Per page, kv-head and of K and V each: e_new is the least e with
+ * |x| <= 448 * 2^e for every finite new element, clamped to [-40, 120] (-40
+ * when all are zero).  The page's exponent e becomes e_new when slot 0 is
+ * among the new tokens (the page starts anew), else the larger of its old
+ * one and e_new; if that raises it, the codes of the slots below the new
+ * tokens are rounded again to the new scale (exact but for subnormals).
+ * Stored codes are x * 2^-e rounded to nearest even from float32;
+ * infinities store as +-448, NaN as NaN.  Nothing else of the pool changes.
+ * Appending the same tokens again gives the same bytes.
+ *   K, V         strided device [n_tokens, h_kv, d] of dtype
+ *   k_weight, freq  as for ssa_qk_rope
+ *   new_start    device int32 [n_seq + 1], non-decreasing, within
+ *                0..n_tokens; tokens outside every sequence are not read
+ *   cached       device int32 [n_seq], tokens already in the cache
+ *   bad_count    device int32, may be NULL: tokens left out
+ */
+SSA_API ssa_status ssa_cache_append(const ssa_append_params* p, const void* K, const void* V,
+                                    const float* k_weight, const double* freq, const int32_t* new_start,
+                                    const int32_t* cached, const int32_t* page_table, uint8_t* k_cache,
+                                    uint8_t* v_cache, float* k_scale, float* v_scale, int32_t* bad_count,
+                                    void* stream);
+
+/* 48 bytes, no padding. */
+typedef struct {
+  int32_t n_seq;
+  int32_t n_q;        /* new tokens per sequence, the last of it                */
+  int32_t max_pages, n_pages, page;
+  int32_t h_q, h_kv;  /* h_q / h_kv in 1..16                                    */
+  int32_t d;          /* 64 or 128                                              */
+  int32_t topk;       /* selected blocks per (new token, kv-head), 0..32; 0:
+                         every key up to the token                              */
+  int32_t window;     /* causal window in keys, 1..4032; 0 when topk = 0        */
+  float scale;        /* logit scale, > 0                                       */
+  int32_t reserved;   /* 0                                                      */
+} ssa_cache_attn_params;
+
+/* Bytes of device workspace ssa_cache_attn needs (0 on invalid arguments, or when it needs none). */
+SSA_API size_t ssa_cache_attn_workspace_size(const ssa_cache_attn_params* p);
+
+/*
+ * Softmax attention of new tokens over the cache: new token i of sequence s
+ * sits at position pos = kv_len[s] - n_q + i and attends, with topk = 0, keys
+ * 0 .. pos; with topk > 0, the keys of its block_idx entries and of the
+ * window pos-window+1 .. pos, each once (blocks are pages; entries are used
+ * and skipped as ssa_sparse_attn does).  kv_len counts the new tokens, whose
+ * keys and values are in the cache already.  A token at a negative position
+ * (kv_len < n_q) has no keys.  A row without keys gives O = 0 and
+ * lse = -inf.  Keys that a row does not attend have no part in it, NaN among
+ * them.  kv_len below 0 counts as 0; beyond max_pages * page it is cut to
+ * that.  Logits, softmax and sums are float32; the probabilities enter
+ * the second product as float16, relative to the row's running maximum.
+ *   Q          device [n_seq, n_q, h_q, d] bf16
+ *   kv_len     device int32 [n_seq]
+ *   block_idx  device int32 [n_seq, n_q, h_kv, topk] (ssa_route_topk's
+ *              layout); NULL when topk = 0
+ *   O          device output [n_seq, n_q, h_q, d] bf16
+ *   lse        device float32 output [n_seq, n_q, h_q], may be NULL: natural
+ *              log of the sum of exp(scale q.k)
+ *   bad_count  device int32, may be NULL: counts block_idx entries and 32-key
+ *              pieces of pages skipped (a piece once for each row group that
+ *              would read it)
+ *   ws         device workspace of ssa_cache_attn_workspace_size(p) bytes;
+ *              calls that may overlap need one each
+ */
+SSA_API ssa_status ssa_cache_attn(const ssa_cache_attn_params* p, const void* Q, const int32_t* page_table,
+                                  const int32_t* kv_len, const uint8_t* k_cache, const uint8_t* v_cache,
+                                  const float* k_scale, const float* v_scale, const int32_t* block_idx,
+                                  void* O, float* lse, int32_t* bad_count, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/*
  * Self-test of the failure path (not part of the layer).  Launches on
  * `stream` one kernel that waits on an mbarrier nothing arrives at, through
  * the bounded wait every kernel of the library uses: after the wait limit

@@ -1,0 +1,593 @@
+"""Serving operators on the GPU against the float64 oracle.
+
+Tolerances (half a unit in the last place u: bf16 2^-8, float32 2^-24, e4m3
+2^-4 relative, e4m3 subnormals 2^-10 of the scale):
+  * rotation: u |y| for the one rounding, plus 2^-18 of the head's largest
+    element for the float32 arithmetic before it (a norm over 128 dims is under
+    24 roundings of 2^-24; the fast cos and sin of bf16 heads are off by at
+    most 2^-20 absolute after the angle's own 2^-22) and 2^-19 for float32;
+  * append: half a code step of the exact value, widened by 2^-16 of the
+    head's largest element for the same float32 arithmetic;
+  * cache attention: u |o| for the bf16 output plus 2^-10 of the largest |v|
+    of the keys: probabilities enter the product as float16 (2^-11 relative,
+    2^-25 absolute against the largest, so 2^-11 + n 2^-25 of sum p|v|/sum p
+    with n <= 2^12 keys here), and 2^-11 is left for ex2.approx (2^-22) and
+    float32 sums;
+  * log-sum-exp: 2^-17 (1 + the largest sum |q_d k_d| scale): float32 sums of
+    128 products and one exp2/log2 each way.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from content_routed_block_ssa_b200 import ssa
+from oracle import serve_oracle as S
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+def rng_of(*key):
+    return np.random.default_rng([sum(map(ord, str(k))) for k in key])
+
+
+def dev(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x))
+    return (t.to(dtype) if dtype is not None else t).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert ssa.ssa_device_error() == 0
+
+
+# ---------------------------------------------------------------- rotation
+
+TD = {"bf16": torch.bfloat16, "f32": torch.float32}
+U = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+FUZZ = {"bf16": 2.0 ** -18, "f32": 2.0 ** -19}
+
+
+def check_rope(got, x, w, f, pos, layout, m, norm, eps, dtype):
+    ref = S.norm(x, w, eps) if norm else np.array(x)
+    big = np.abs(ref).max(-1, keepdims=True) * max(abs(m), 1.0)
+    ref = S.rotate(ref, f, pos, layout, m)
+    assert (np.abs(f64(got) - ref) <= U[dtype] * np.abs(ref) + FUZZ[dtype] * big).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,layout", [(128, 128, "half"), (128, 128, "pairs"), (128, 96, "half"), (64, 16, "pairs"),
+                                          (64, 64, "half"), (64, 48, "half"), (128, 32, "pairs"), (128, 0, "half")])
+@pytest.mark.parametrize("T,hq,hkv", [(1, 1, 1), (3, 7, 2), (37, 32, 8)])
+def test_rope(dtype, d, rot, layout, T, hq, hkv):
+    r = rng_of(dtype, d, rot, layout, T)
+    # a joint projection with a gap behind it: strided tokens
+    x = dev(r.normal(size=(T, hq + 2 * hkv + 1, d)) * r.choice([0.1, 1, 30], size=(T, 1, 1)), TD[dtype])
+    q, k = x[:, :hq], x[:, hq:hq + hkv]
+    qw, kw = dev(r.normal(size=d), torch.float32), dev(1 + r.normal(size=d), torch.float32)
+    f, _ = ssa.rope_frequencies(max(rot, 2), 10000.0)
+    f = f[:rot // 2]
+    pos = r.integers(-5, 1 << 20, size=T)
+    qo, ko = torch.full_like(q, 7.0).contiguous(), torch.full_like(k, 7.0).contiguous()
+    p = ssa.make_rope_params(T, hq, hkv, d, rot, layout, dtype, True, 1e-5, 1.25, q_stride=x.stride(0), k_stride=x.stride(0))
+    before = x.clone()
+    ssa.ssa_qk_rope(p, q, k, qw, kw, f.cuda(), dev(pos, torch.int32), qo, ko)
+    ok()
+    assert torch.equal(x, before)
+    check_rope(qo, f64(q), f64(qw), f.numpy(), pos, layout, 1.25, True, 1e-5, dtype)
+    check_rope(ko, f64(k), f64(kw), f.numpy(), pos, layout, 1.25, True, 1e-5, dtype)
+    # in place, without the norm
+    p = ssa.make_rope_params(T, hq, hkv, d, rot, layout, dtype, False, q_stride=x.stride(0), k_stride=x.stride(0),
+                             q_out_stride=x.stride(0), k_out_stride=x.stride(0))
+    ssa.ssa_qk_rope(p, q, k, qw, kw, f.cuda(), dev(pos, torch.int32), q, k)
+    ok()
+    check_rope(q, f64(before[:, :hq]), None, f.numpy(), pos, layout, 1.0, False, 0, dtype)
+    check_rope(k, f64(before[:, hq:hq + hkv]), None, f.numpy(), pos, layout, 1.0, False, 0, dtype)
+    assert torch.equal(x[:, hq + hkv:], before[:, hq + hkv:])      # values and gap untouched
+
+
+def test_rope_many_tokens_and_far_positions():
+    """More tokens than one wave of warps, positions up to 2^31 - 1: a
+    float32 angle would be off by many turns."""
+    T, d = 3001, 64
+    r = rng_of("far")
+    q, k = dev(r.normal(size=(T, 2, d)), torch.float32), dev(r.normal(size=(T, 1, d)), torch.float32)
+    f, m = ssa.rope_frequencies(d, 500000.0, "blend", 32.0, 8192.0)
+    pos = r.integers(-(1 << 31), 1 << 31, size=T)
+    pos[:3] = [(1 << 31) - 1, -(1 << 31), 0]
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    p = ssa.make_rope_params(T, 2, 1, d, dtype="f32", norm=False, mscale=m)
+    ssa.ssa_qk_rope(p, q, k, None, None, f.cuda(), dev(pos, torch.int32), qo, ko)
+    ok()
+    # 2^-53 relative in the frequency is 2^-22 turns of 2^31 positions at one
+    # radian each: allow 2 pi 2^-23 of the pair besides the float32 part
+    ref = S.rotate(f64(q), f.numpy(), pos, "half", m)
+    big = np.abs(f64(q)).max(-1, keepdims=True) * m
+    assert (np.abs(f64(qo) - ref) <= U["f32"] * np.abs(ref) + (FUZZ["f32"] + 2.0 ** -20) * big).all()
+
+
+def test_rope_leaves_unrotated_infinities_and_keeps_heads_apart():
+    x = torch.ones(2, 3, 128, device="cuda")
+    x[0, 0, 100] = math.inf
+    x[1, 1, 3] = math.nan
+    f = ssa.rope_frequencies(64)[0].cuda()
+    p = ssa.make_rope_params(2, 2, 1, 128, 64, dtype="f32", norm=False, q_stride=384, k_stride=384)
+    q, k = torch.empty(2, 2, 128, device="cuda"), torch.empty(2, 1, 128, device="cuda")
+    ssa.ssa_qk_rope(p, x[:, :2], x[:, 2:], None, None, f, torch.tensor([5, 9], dtype=torch.int32, device="cuda"), q, k)
+    ok()
+    assert q[0, 0, 100] == math.inf and torch.isfinite(q[0, 0, :100]).all() and torch.isfinite(q[0, 1]).all()
+    assert q[1, 1].isnan().nonzero().flatten().tolist() == [3, 35] and torch.isfinite(k).all()
+
+
+# ---------------------------------------------------------------- append
+
+def pool(r, n_pages, h, page, d):
+    codes = r.integers(0, 256, size=(2, n_pages, h, page, d)).astype(np.uint8)
+    codes[(codes & 127) == 127] = 0
+    scale = 2.0 ** r.integers(-9, -5, size=(2, n_pages, h))
+    return codes, scale
+
+
+def run_append(p, K, V, w, f, cu, have, table, codes, scale):
+    kc, vc = dev(codes[0]), dev(codes[1])
+    ks, vs = dev(scale[0], torch.float32), dev(scale[1], torch.float32)
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (p, K, V, w, f, dev(cu, torch.int32), dev(have, torch.int32), dev(table, torch.int32), kc, vc, ks, vs)
+    ssa.ssa_cache_append(*args, bad)
+    ok()
+    one = [t.clone() for t in (kc, vc, ks, vs)]
+    ssa.ssa_cache_append(*args)                     # the same tokens again: the same bytes
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(one, (kc, vc, ks, vs)))
+    return (kc, vc, ks, vs), int(bad)
+
+
+def check_codes(got_c, got_s, ref_c, ref_s, x, cu, have, table, page, old_c):
+    """Scales equal; codes equal but where the exact value is too near a
+    border between codes for float32 to tell; nothing else changed."""
+    got_c, got_s = got_c.cpu().numpy(), f64(got_s)
+    assert np.array_equal(got_s, ref_s)
+    differ = np.argwhere(got_c != ref_c)
+    where = {}
+    for s in range(len(have)):
+        for o, row in enumerate(range(cu[s], cu[s + 1])):
+            pos = have[s] + o
+            if have[s] >= 0 and pos // page < table.shape[1] and 0 <= table[s, pos // page] < len(ref_c):
+                where[(table[s, pos // page], pos % page)] = row
+    val = S.e4m3_values()
+    for pid, h, sl, i in differ:
+        row = where[(pid, sl)]                      # only appended slots may differ
+        step = max(2.0 ** -4 * abs(x[row, h, i]), 2.0 ** -10 * ref_s[pid, h])
+        off = abs(val[got_c[pid, h, sl, i]] * ref_s[pid, h] - x[row, h, i])
+        assert off <= step * (1 + 2.0 ** -8) + 2.0 ** -16 * np.abs(x[row, h]).max()
+    assert len(differ) <= 1 + 1e-3 * sum(cu[s + 1] - cu[s] for s in range(len(have))) * ref_c.shape[1] * ref_c.shape[3]
+
+
+def append_case(r, n_seq, page, news, haves):
+    cu = np.concatenate([[0], np.cumsum(news)])
+    pages = [(h + n + page - 1) // page for h, n in zip(haves, news)]
+    width = max(max(pages), 1)
+    ids = r.permutation(sum(pages) + 2)
+    table, at = np.full((n_seq, width), -1), 0
+    for s, n in enumerate(pages):
+        table[s, :n] = ids[at:at + n]
+        at += n
+    return cu, table, len(ids)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,page,rot,layout", [(128, 64, 128, "half"), (64, 128, 48, "pairs"), (128, 128, 64, "half"),
+                                               (64, 64, 0, "half")])
+@pytest.mark.parametrize("news,haves", [
+    ([1], [0]), ([1, 1, 1, 1], [0, 63, 64, 130]),             # decode: fresh page, last slot, page border
+    ([3, 0, 17, 1, 5], [62, 5, 120, 0, 127]),                 # ragged, an empty sequence, pages that end inside
+    ([200], [0]), ([131, 1, 70], [30, 64, 1]),                # prompts over several pages
+    ([0, 0], [3, 0]),
+])
+def test_append(dtype, d, page, rot, layout, news, haves):
+    r = rng_of(dtype, d, page, rot, news, haves)
+    h = 3
+    cu, table, n_pages = append_case(r, len(news), page, news, haves)
+    T = int(cu[-1]) + 4                                       # tokens behind the last sequence are not used
+    x = dev(r.normal(size=(T, 2 * h, d)) * 2.0 ** r.integers(-3, 4, size=(T, 1, 1)), TD[dtype])
+    x[cu[-1]:] = math.nan
+    K, V = x[:, :h], x[:, h:]
+    w = dev(1 + 0.2 * r.normal(size=d), torch.float32)
+    f, _ = ssa.rope_frequencies(max(rot, 2))
+    f = f[:rot // 2]
+    codes, scale = pool(r, n_pages, h, page, d)
+    p = ssa.make_append_params(T, len(news), table.shape[1], n_pages, page, h, d, rot, layout, dtype, True, 1e-6, 1.0,
+                               k_stride=x.stride(0), v_stride=x.stride(0))
+    (kc, vc, ks, vs), bad = run_append(p, K, V, w, f.cuda(), cu, haves, table, codes, scale)
+    assert bad == 0
+    pos = np.concatenate([np.arange(hv, hv + n) for hv, n in zip(haves, news)] + [np.zeros(4, int)])
+    kx = f64(K)
+    kx[cu[-1]:] = 0
+    kx = S.rotate(S.norm(kx, f64(w), 1e-6), f.numpy(), pos, layout)
+    for got, gs, xx, j in ((kc, ks, kx, 0), (vc, vs, f64(V), 1)):
+        rc, rs, _ = S.append(xx, cu, haves, table, page, codes[j], scale[j])
+        check_codes(got, gs, rc, rs, xx, cu, haves, table, page, codes[j])
+
+
+@pytest.mark.parametrize("few", [True, False])
+def test_append_plain_values_are_bit_exact_and_survive_growth(few):
+    """No norm, no rotation: the codes are the rounding of the inputs, bit
+    for bit, through a growing scale, infinities, NaN and zeros."""
+    r = rng_of("grow")
+    page, d, h = 64, 128, 2
+    n = 40 if not few else 8
+    codes, scale = pool(r, 3, h, page, d)
+    scale[:] = 2.0 ** -12
+    x = r.normal(size=(n, h, d)).astype(np.float32)
+    x[0, 0, :4] = [np.inf, -np.inf, np.nan, 0.0]
+    x[n - 1, 1] = 1e30                                        # far above the page's old scale
+    x[1, 1, 0] = 3e-39                                        # a float32 subnormal
+    K = dev(x)
+    V = torch.zeros_like(K)
+    cu, have, table = np.array([0, n]), np.array([20]), np.array([[2]])
+    if few:                                                   # many sequences without tokens: the decode kernel
+        cu, have, table = np.array([0] * 4 + [n]), np.array([5, 5, 5, 20]), np.array([[0], [0], [1], [2]])
+    p = ssa.make_append_params(n, len(have), 1, 3, page, h, d, 0, "half", "f32", False)
+    (kc, vc, ks, vs), bad = run_append(p, K, V, None, None, cu, have, table, codes, scale)
+    rc, rs, _ = S.append(x.astype(np.float64), cu, have, table, page, codes[0], scale[0])
+    got = kc.cpu().numpy()
+    nan = (rc & 127) == 127
+    assert np.array_equal(got[~nan], rc[~nan]) and ((got[nan] & 127) == 127).all()
+    assert np.array_equal(f64(ks), rs) and bad == 0
+    assert rs[2, 1] == 2.0 ** S.exponent([1e30])
+    rv, rvs, _ = S.append(np.zeros((n, h, d)), cu, have, table, page, codes[1], scale[1])
+    assert np.array_equal(vc.cpu().numpy(), rv) and np.array_equal(f64(vs), rvs) and (rvs[2] == 2.0 ** -12).all()
+
+
+def test_append_fresh_page_of_zeros_and_tiny_values():
+    K = torch.zeros(2, 1, 64, device="cuda")
+    V = torch.full((2, 1, 64), 1e-20, device="cuda")
+    codes, scale = pool(rng_of("z"), 1, 1, 64, 64)
+    p = ssa.make_append_params(2, 1, 1, 1, 64, 1, 64, 0, "half", "f32", False)
+    (kc, vc, ks, vs), _ = run_append(p, K, V, None, None, np.array([0, 2]), np.array([0]), np.array([[0]]), codes, scale)
+    assert ks.item() == vs.item() == 2.0 ** -40
+    assert not (kc[0, 0, :2] & 127).any() and not (vc[0, 0, :2] & 127).any()
+    assert np.array_equal(kc[0, 0, 2:].cpu().numpy(), codes[0][0, 0, 2:])   # the rest of the page as it was
+
+
+@pytest.mark.parametrize("n", [2, 150])
+def test_append_leaves_out_what_does_not_fit(n):
+    """Pages outside the pool, negative lengths, tokens past the table and
+    decreasing offsets are left out and counted; nothing else is written."""
+    r = rng_of("bad", n)
+    page, d, h = 64, 64, 2
+    x = dev(r.normal(size=(5 * n, 2 * h, d)), torch.bfloat16)
+    cu = np.array([0, n, 2 * n, 3 * n, 4 * n, 5 * n])
+    have = np.array([0, -1, 3 * page - 1, 10, 2 * page])      # the third has one slot left in the table
+    table = np.array([[7, 7, 7], [0, 1, 2], [-1, -1, 5], [-9, 1 << 30, 6], [0, 1, 2]])
+    codes, scale = pool(r, 7, h, page, d)
+    p = ssa.make_append_params(5 * n, 5, 3, 7, page, h, d, 0, "half", "bf16", False, k_stride=x.stride(0),
+                               v_stride=x.stride(0))
+    (kc, vc, ks, vs), bad = run_append(p, x[:, :h], x[:, h:], None, None, cu, have, table, codes, scale)
+    for got, gs, xx, j in ((kc, ks, f64(x[:, :h]), 0), (vc, vs, f64(x[:, h:]), 1)):
+        rc, rs, rb = S.append(xx, cu, have, table, page, codes[j], scale[j])
+        assert np.array_equal(got.cpu().numpy(), rc) and np.array_equal(f64(gs), rs) and rb == bad
+    # offsets that decrease or leave the rows: nothing out of bounds is read
+    for odd in ([0, 4 * n, n, 1 << 30, -5, 5 * n], [-3, -2, -1, 9 * n, 9 * n, 9 * n], [5 * n] * 6):
+        run_append(p, x[:, :h], x[:, h:], None, None, np.array(odd), have, table, codes, scale)
+
+
+def test_append_many_sequences():
+    """More sequences than one 32-way search step covers, some without tokens."""
+    r = rng_of("many")
+    page, d, h, n_seq = 64, 64, 1, 1100
+    news = r.integers(0, 4, size=n_seq)
+    news[500] = 90
+    haves = r.integers(0, 130, size=n_seq)
+    cu, table, n_pages = append_case(r, n_seq, page, news, haves)
+    x = r.normal(size=(int(cu[-1]), h, d)).astype(np.float32)
+    codes, scale = pool(r, n_pages, h, page, d)
+    p = ssa.make_append_params(int(cu[-1]), n_seq, table.shape[1], n_pages, page, h, d, 0, "half", "f32", False)
+    (kc, vc, ks, vs), bad = run_append(p, dev(x), dev(-x), None, None, cu, haves, table, codes, scale)
+    rc, rs, _ = S.append(x.astype(np.float64), cu, haves, table, page, codes[0], scale[0])
+    assert np.array_equal(kc.cpu().numpy(), rc) and np.array_equal(f64(ks), rs) and bad == 0
+
+
+# ---------------------------------------------------------------- attention over the cache
+
+def cache_case(r, lens, n_q, h_kv, G, d, page, topk=0):
+    n = len(lens)
+    pages = [max((L + page - 1) // page, 0) for L in lens]
+    width = max(max(pages), 1) + 1
+    ids = r.permutation(sum(pages) + 1)
+    table, at = np.full((n, width), -1), 0
+    for s, c in enumerate(pages):
+        table[s, :c] = ids[at:at + c]
+        at += c
+    codes, scale = pool(r, len(ids), h_kv, page, d)
+    codes = S.to_e4m3(100 * r.normal(size=codes.shape))
+    scale = 2.0 ** r.integers(-9, -4, size=scale.shape)
+    q = dev(r.normal(size=(n, n_q, h_kv * G, d)), torch.bfloat16)
+    idx = None
+    if topk:
+        idx = np.full((n, n_q, h_kv, topk), -1)
+        for s in range(n):
+            for i in range(n_q):
+                nvis = max(lens[s] - n_q + i + 1, 0) // page
+                for h in range(h_kv):
+                    c = np.sort(r.permutation(nvis)[:topk])
+                    idx[s, i, h, :len(c)] = c
+    return table, codes, scale, q, idx
+
+
+def run_cache(q, lens, table, codes, scale, page, idx=None, window=0, sm_scale=None, bad=None, stream=None):
+    n, n_q, h_q, d = q.shape
+    _, n_pages, h_kv = scale.shape
+    p = ssa.make_cache_attn_params(n, n_q, table.shape[1], n_pages, page, h_q, h_kv, d,
+                                   0 if idx is None else idx.shape[-1], window, sm_scale)
+    ws = ssa.byte_buffer(ssa.ssa_cache_attn_workspace_size(p))
+    ws.fill_(255)                                             # NaN: nothing of it may count
+    o = torch.full_like(q, math.nan)
+    lse = torch.full((n, n_q, h_q), math.nan, device="cuda")
+    ssa.ssa_cache_attn(p, q, dev(table, torch.int32), dev(lens, torch.int32), dev(codes[0]), dev(codes[1]),
+                       dev(scale[0], torch.float32), dev(scale[1], torch.float32),
+                       None if idx is None else dev(idx, torch.int32), o, lse, bad, ws, stream)
+    ok()
+    return o, lse, p
+
+
+def check_cache(o, lse, q, lens, table, codes, scale, page, idx=None, window=0, sm_scale=None):
+    d = q.shape[-1]
+    sm = 1 / math.sqrt(d) if sm_scale is None else sm_scale
+    ro, rl = S.cache_attention(f64(q), table, lens, page, codes[0], codes[1], scale[0], scale[1], sm, idx, window)
+    o, lse = f64(o), f64(lse)
+    vmax = 448.0 * scale[1].max() if codes[1].size else 1.0
+    qmax = np.abs(f64(q)).sum(-1).max() * 448.0 * scale[0].max() * sm
+    assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * vmax).all()
+    empty = np.isinf(rl)
+    assert np.array_equal(np.isinf(lse), empty) and (o[empty] == 0).all()
+    assert (np.abs(lse[~empty] - rl[~empty]) <= 2.0 ** -17 * (1 + qmax)).all()
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128), (128, 128), (64, 64)])
+@pytest.mark.parametrize("h_kv,G,n_q", [(2, 4, 1), (1, 8, 3), (3, 1, 1), (2, 3, 5), (1, 16, 2), (1, 2, 37)])
+@pytest.mark.parametrize("lens", [[1], [0, 31, 32, 33, 64], [700, 1, 129], [40, -7, 2]])
+def test_cache_attention(d, page, h_kv, G, n_q, lens):
+    r = rng_of(d, page, h_kv, G, n_q, lens)
+    table, codes, scale, q, _ = cache_case(r, lens, n_q, h_kv, G, d, page)
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page)
+    check_cache(o, lse, q, lens, table, codes, scale, page)
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128)])
+def test_cache_attention_split_over_a_long_axis(d, page):
+    r = rng_of("long", d)
+    lens = [3000, 4096, 1500]
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 2, 4, d, page)
+    o, lse, p = run_cache(q, lens, table, codes, scale, page)
+    assert ssa.ssa_cache_attn_workspace_size(p) > 0            # several splits, joined
+    check_cache(o, lse, q, lens, table, codes, scale, page)
+    # a table far wider than the lengths: most splits are empty
+    wide = np.full((3, 4096), -1)
+    wide[:, :table.shape[1]] = table
+    o2, lse2, _ = run_cache(q, lens, wide, codes, scale, page)
+    check_cache(o2, lse2, q, lens, table, codes, scale, page)
+
+
+@pytest.mark.parametrize("d,page,window", [(128, 64, 64), (64, 128, 200), (128, 128, 1), (64, 64, 333)])
+@pytest.mark.parametrize("h_kv,G,n_q,topk", [(2, 4, 1, 8), (1, 8, 3, 32), (2, 1, 2, 1)])
+def test_cache_attention_over_selected_blocks(d, page, window, h_kv, G, n_q, topk):
+    r = rng_of("sel", d, page, window, h_kv, n_q, topk)
+    lens = [2500, 64, 1, 0, 129, 640]
+    table, codes, scale, q, idx = cache_case(r, lens, n_q, h_kv, G, d, page, topk)
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, idx, window)
+    check_cache(o, lse, q, lens, table, codes, scale, page, idx, window)
+    # out-of-order, repeated, invisible and negative entries are skipped and counted
+    idx[0, 0, 0, :] = -1
+    row = [5, 5, 3, 1 << 29, -4, 9, 2400 // page + 5][:topk]
+    idx[0, 0, 0, :len(row)] = row
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, idx, window, bad=bad)
+    check_cache(o, lse, q, lens, table, codes, scale, page, idx, window)
+    _, skipped = S.used_blocks(idx[0, 0, 0], 2500 - n_q, page)
+    assert int(bad) == skipped
+
+
+def test_cache_attention_equals_the_layer_on_the_same_keys():
+    """With values that the codes hold exactly, decode over the cache is the
+    layer's decode (route, then attend) over dense keys: same selection, same
+    output to the rounding of the two paths."""
+    from content_routed_block_ssa_b200.workload import Workload, make_inputs, problem_dict
+    w = Workload("serve", 77, 3, 2048, 8, 2, 128, "bf16", 64, "diag", 8, 128, 4, "per_seq", decode=True)
+    Q, K, V, _ = make_inputs(w, "cpu")
+    b, n, h, d = K.shape
+    kc, vc = S.to_e4m3(K.float().numpy() * 16), S.to_e4m3(V.float().numpy() * 16)
+    val = S.e4m3_values() / 16
+    K, V = dev(val[kc], torch.bfloat16), dev(val[vc], torch.bfloat16)
+    p = ssa.make_params(**problem_dict(w))
+    Q = Q.cuda()
+    tab = torch.empty(ssa.summary_shapes(p)[2], dtype=torch.bfloat16, device="cuda")
+    ssa.ssa_block_summary(p, K, None, None, tab)
+    idx = torch.empty(ssa.idx_shape(p), dtype=torch.int32, device="cuda")
+    ssa.ssa_route_topk(p, Q, None, None, tab, idx)
+    O, lse = torch.empty_like(Q), torch.empty(b, 1, w.h_q, device="cuda")
+    ssa.ssa_sparse_attn(p, Q, K, V, idx, O, lse)
+    nb = n // 64
+    paged = lambda c: c.reshape(b, nb, 64, h, d).transpose(0, 1, 3, 2, 4).reshape(b * nb, h, 64, d)  # noqa: E731
+    table = np.arange(b * nb).reshape(b, nb)
+    scale = np.full((2, b * nb, h), 1 / 16)
+    o, l2, _ = run_cache(Q, [n] * b, table, np.stack([paged(kc), paged(vc)]), scale, 64, idx.cpu().numpy(), w.window)
+    check_cache(o, l2, Q, [n] * b, table, np.stack([paged(kc), paged(vc)]), scale, 64, idx.cpu().numpy(), w.window)
+    assert (o.float() - O.float()).abs().max() <= 2 * 2.0 ** -8 * O.float().abs().max() + 2.0 ** -9 * V.float().abs().max()
+    assert (l2 - lse).abs().max() <= 1e-4 * lse.abs().max()
+
+
+def test_cache_attention_ignores_what_it_does_not_attend():
+    """NaN codes behind a sequence's end, in other pages and in later new
+    tokens have no part in a row; a NaN key or value that it attends does."""
+    r = rng_of("nan")
+    d, page, n_q, lens = 128, 64, 4, [100, 70]
+    table, codes, scale, q, _ = cache_case(r, lens, n_q, 2, 4, d, page)
+    clean_o, clean_l, _ = run_cache(q, lens, table, codes, scale, page)
+    dirty = codes.copy()
+    for s, L in enumerate(lens):
+        dirty[:, table[s, L // page], :, L % page:] = 127                    # behind the end
+    unused = sorted(set(range(codes.shape[1])) - set(table.flatten()))
+    dirty[:, unused] = 255
+    o, lse, _ = run_cache(q, lens, table, dirty, scale, page)
+    assert torch.equal(o, clean_o) and torch.equal(lse, clean_l)
+    dirty = codes.copy()
+    dirty[1, table[0, 98 // page], 1, 98 % page, 17] = 127                   # one value of new token 2
+    o, lse, _ = run_cache(q, lens, table, dirty, scale, page)
+    assert torch.equal(lse, clean_l)
+    nan = o.isnan()
+    want = torch.zeros_like(nan)
+    want[0, 2:, 4:, 17] = True                                               # tokens 2, 3 of kv-head 1's group
+    assert torch.equal(nan, want) and torch.equal(o[~nan], clean_o[~nan])
+    dirty = codes.copy()
+    dirty[0, table[0, 98 // page], 1, 98 % page, 17] = 127                   # the same of a key
+    o, lse, _ = run_cache(q, lens, table, dirty, scale, page)
+    assert torch.equal(lse.isnan(), want.any(-1)) and torch.equal(o.isnan(), want.any(-1, keepdim=True).expand_as(o))
+    assert torch.equal(o[~o.isnan()], clean_o[~o.isnan()])
+
+
+def test_cache_attention_pages_outside_the_pool_are_left_out():
+    r = rng_of("badpage")
+    d, page, lens = 64, 64, [400, 1000]
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 2, 2, d, page)
+    table[0, 2], table[0, 3], table[1, 5] = -3, 1 << 30, codes.shape[1]
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, bad=bad)
+    check_cache(o, lse, q, lens, table, codes, scale, page)
+    assert int(bad) == 3 * 2 * 2                              # pieces of 32 keys, for each of two kv-heads
+    table[:] = -1                                             # nothing left: every row is empty
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page)
+    assert not o.any() and (lse == -math.inf).all()
+    # lengths beyond the table are cut to it
+    table, codes, scale, q, _ = cache_case(r, [128], 1, 2, 2, d, page)
+    o, lse, _ = run_cache(q, [1 << 30], table[:, :2], codes, scale, page)
+    check_cache(o, lse, q, [128], table[:, :2], codes, scale, page)
+
+
+def test_cache_attention_scales_and_queries_of_very_different_size():
+    """Pages whose value scales differ by 2^40, rows whose elements differ by
+    2^20: the running reference keeps every product in range."""
+    r = rng_of("range")
+    d, page, lens = 128, 64, [320]
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 1, 8, d, page)
+    scale[1, table[0, 1]] = 2.0 ** 30
+    scale[1, table[0, 3]] = 2.0 ** -40
+    scale[0, table[0, 2]] = 2.0 ** -12
+    q[..., ::7] *= 2.0 ** -20
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page)
+    check_cache(o, lse, q, lens, table, codes, scale, page)
+    # the same with the large page out of reach: the tiny page's rows count in full
+    scale[1, table[0, 1]] = 2.0 ** -40
+    o, lse, _ = run_cache(q * 64, lens, table, codes, scale, page)
+    check_cache(o, lse, q * 64, lens, table, codes, scale, page)
+    o, lse, _ = run_cache(q * 0, lens, table, codes, scale, page)
+    check_cache(o, lse, q * 0, lens, table, codes, scale, page)
+
+
+# ---------------------------------------------------------------- together
+
+def test_a_serving_loop_matches_attention_over_everything():
+    """Prompt, then decode steps: rotate, append, attend; each step's output
+    against the oracle over the cache as it stands, and the cache against the
+    exact keys to its rounding."""
+    r = rng_of("loop")
+    n_seq, h_q, h_kv, d, page, width = 3, 8, 2, 128, 64, 6
+    f, m = ssa.rope_frequencies(d, 10000.0, "blend", 4.0, 128.0)
+    fd = f.cuda()
+    qw, kw = dev(1 + 0.1 * r.normal(size=d), torch.float32), dev(1 + 0.1 * r.normal(size=d), torch.float32)
+    table = r.permutation(n_seq * width).reshape(n_seq, width)
+    td = dev(table, torch.int32)
+    codes, scale = pool(r, n_seq * width, h_kv, page, d)
+    kc, vc, ks, vs = dev(codes[0]), dev(codes[1]), dev(scale[0], torch.float32), dev(scale[1], torch.float32)
+    have = np.zeros(n_seq, int)
+    keys = [[] for _ in range(n_seq)]
+    for step in range(6):
+        news = [5, 130, 64] if step == 0 else [1] * n_seq
+        n_q = 1
+        cu = np.concatenate([[0], np.cumsum(news)])
+        T = int(cu[-1])
+        x = dev(r.normal(size=(T, h_q + 2 * h_kv, d)), torch.bfloat16)
+        q, k, v = x[:, :h_q], x[:, h_q:h_q + h_kv], x[:, h_q + h_kv:]
+        pos = np.concatenate([np.arange(a, a + n) for a, n in zip(have, news)])
+        qo, ko = torch.empty(T, h_q, d, device="cuda", dtype=torch.bfloat16), torch.empty(T, h_kv, d, device="cuda", dtype=torch.bfloat16)
+        rp = ssa.make_rope_params(T, h_q, h_kv, d, mscale=m, q_stride=x.stride(0), k_stride=x.stride(0))
+        ssa.ssa_qk_rope(rp, q, k, qw, kw, fd, dev(pos, torch.int32), qo, ko)
+        ap = ssa.make_append_params(T, n_seq, width, n_seq * width, page, h_kv, d, mscale=m, k_stride=x.stride(0),
+                                    v_stride=x.stride(0))
+        ssa.ssa_cache_append(ap, k, v, kw, fd, dev(cu, torch.int32), dev(have, torch.int32), td, kc, vc, ks, vs)
+        exact = S.rotate(S.norm(f64(k), f64(kw)), f.numpy(), pos, "half", m)
+        for s in range(n_seq):
+            keys[s] += list(exact[cu[s]:cu[s + 1]])
+        have = have + news
+        last = qo[dev(cu[1:] - 1)].view(n_seq, n_q, h_q, d).contiguous()
+        cs = np.stack([kc.cpu().numpy(), vc.cpu().numpy()])
+        sc = np.stack([f64(ks), f64(vs)])
+        o, lse, _ = run_cache(last, have, table, cs, sc, page)
+        check_cache(o, lse, last, have, table, cs, sc, page)
+    val = S.e4m3_values()
+    for s in range(n_seq):
+        for j, x in enumerate(keys[s]):
+            pid, sl = table[s, j // page], j % page
+            got = val[cs[0, pid, :, sl]] * sc[0, pid][:, None]
+            # a key stored before its page's scale grew was rounded twice, the second time only where subnormal
+            assert (np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * sc[0, pid][:, None] + 2.0 ** -16 * np.abs(x).max()).all()
+
+
+def test_operators_run_on_a_side_stream_and_replay_from_a_graph():
+    r = rng_of("graph")
+    lens, page, d = [500, 1300], 64, 128
+    table, codes, scale, q, idx = cache_case(r, lens, 1, 2, 4, d, page, 4)
+    ref, ref_l, p = run_cache(q, lens, table, codes, scale, page)
+    td, ld = dev(table, torch.int32), dev(lens, torch.int32)
+    kc, vc, ks, vs = dev(codes[0]), dev(codes[1]), dev(scale[0], torch.float32), dev(scale[1], torch.float32)
+    ws = ssa.byte_buffer(ssa.ssa_cache_attn_workspace_size(p))
+    o, lse = torch.zeros_like(q), torch.zeros(2, 1, 8, device="cuda")
+    x = dev(r.normal(size=(2, 4, d)), torch.bfloat16)
+    f = ssa.rope_frequencies(d)[0].cuda()
+    cu, have = dev([0, 1, 2], torch.int32), dev(np.array(lens) - 1, torch.int32)
+    rp = ssa.make_rope_params(2, 2, 2, d, q_stride=x.stride(0), k_stride=x.stride(0))
+    ap = ssa.make_append_params(2, 2, td.shape[1], kc.shape[0], page, 2, d, k_stride=x.stride(0), v_stride=x.stride(0))
+    qo, ko = torch.empty(2, 2, d, device="cuda", dtype=torch.bfloat16), torch.empty(2, 2, d, device="cuda", dtype=torch.bfloat16)
+
+    def step(stream=None):
+        ssa.ssa_qk_rope(rp, x[:, :2], x[:, 2:], None, None, f, have, qo, ko, stream)
+        ssa.ssa_cache_append(ap, x[:, :2], x[:, 2:], None, f, cu, have, td, kc, vc, ks, vs, None, stream)
+        ssa.ssa_cache_attn(p, q, td, ld, kc, vc, ks, vs, None, o, lse, ws=ws, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    torch.cuda.current_stream().wait_stream(side)
+    ok()
+    first, first_l, rot = o.clone(), lse.clone(), qo.clone()
+    cs, sc = np.stack([kc.cpu().numpy(), vc.cpu().numpy()]), np.stack([f64(ks), f64(vs)])
+    check_cache(first, first_l, q, lens, table, cs, sc, page)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    o.zero_(), lse.zero_(), qo.zero_(), ws.fill_(255)
+    x.copy_(x.flip(0))
+    g.replay()
+    ok()
+    assert not torch.equal(qo, rot) and not torch.equal(o, first)      # the new inputs are used
+    cs, sc = np.stack([kc.cpu().numpy(), vc.cpu().numpy()]), np.stack([f64(ks), f64(vs)])
+    check_cache(o, lse, q, lens, table, cs, sc, page)
+    again = o.clone()
+    g.replay()
+    ok()
+    assert torch.equal(o, again)                                       # and the same bytes each time
+
+
+def test_results_do_not_depend_on_the_run():
+    r = rng_of("same")
+    lens = [2000, 77, 1024]
+    table, codes, scale, q, _ = cache_case(r, lens, 2, 2, 4, 128, 64)
+    a, al, _ = run_cache(q, lens, table, codes, scale, 64)
+    b, bl, _ = run_cache(q, lens, table, codes, scale, 64)
+    assert torch.equal(a, b) and torch.equal(al, bl)

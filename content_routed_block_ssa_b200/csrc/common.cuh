@@ -38,6 +38,10 @@ enum WaitSite : uint32_t {
   SITE_WIN_SOFTMAX = 0x503,
   SITE_WIN_SMEM = 0x504,       // the aligned shared-memory layout did not fit its allocation
   SITE_CACHE_FULL = 0x601,     // attention over the paged cache: a piece of a page
+  SITE_PROMPT_PRODUCER = 0x611,   // attention over packed prompts
+  SITE_PROMPT_MMA = 0x612,
+  SITE_PROMPT_SOFTMAX = 0x613,
+  SITE_PROMPT_SMEM = 0x614,    // the aligned shared-memory layout did not fit its allocation
   SITE_SELFTEST = 0x7F1,       // the failure-path self-test: a wait that nothing completes
 };
 

@@ -235,6 +235,10 @@ struct CacheAttnArgs {
 size_t cache_attn_ws(const ssa_cache_attn_params& p);
 cudaError_t launch_cache_attn(const ssa_cache_attn_params& p, const CacheAttnArgs& a, const LaunchCtx& c);
 
+cudaError_t launch_prompt_attn(const ssa_prompt_params& p, const void* Q, const void* K, const void* V,
+                               const int32_t* q_start, const int32_t* kv_start, void* O, float* lse,
+                               const LaunchCtx& c);
+
 // One CTA whose bounded wait never completes (the failure-path self-test).
 cudaError_t launch_selftest_wait(const LaunchCtx& c);
 

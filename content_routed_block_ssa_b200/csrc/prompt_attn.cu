@@ -1,0 +1,526 @@
+// Causal attention over packed prompts of different lengths, grouped heads.
+//
+// A block takes one unit: two tensor-core tiles of 128 rows, each of
+// QT = 128 / G consecutive queries x the G query heads of one kv-head, so the
+// keys and values of a kv-head are read once for its whole group.  Per step of
+// 128 keys and tile: S = Q K^T (tcgen05, into tensor memory), a softmax of one
+// row per thread, P = 2^(s - m) in bf16 over the S columns, O += P V with P
+// as the A operand from tensor memory.  The two tiles take turns: while the
+// softmax warps of one work, the tensor core runs the other's products.
+//
+// Per step and tile both products take 2 x 512 tensor-core clocks (d = 128)
+// and the 128 x 128 exponentials 1024 clocks of the four special-function
+// units: the two bound each other, which is why everything else of the softmax
+// is kept short: one thread owns a row (no shuffles), packed float32 pairs,
+// and the output is rescaled only when a row's maximum has grown by more
+// than 2^8 (any reference gives the same ratios, and 2^8 leaves the sums and
+// the bf16 probabilities far from overflow).
+//
+// Units are numbered by the packed query rows (floor(q_start / rows) + s and
+// up: sequence ranges never meet); the grid starts at the last ones, whose
+// causal prefix is the longest.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace ssa {
+namespace {
+
+template <int D>
+struct PromptShape {
+  static constexpr int ROW = 128;                     // bytes of a 64-dim swizzled row
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE = 128 * ROW * HALVES;     // 128 rows (queries x heads, or keys)
+  static constexpr int SLOTS = D == 128 ? 5 : 8;      // ring of K and V tiles
+  static constexpr int BARS = 2 * TILE + SLOTS * TILE;
+  static constexpr int NBAR = 1 + 2 * SLOTS + 2 + 2 + 2 + 1;
+  static constexpr int USED = BARS + NBAR * 8 + 16;
+  static constexpr int SMEM = USED + 1024 < 232448 ? USED + 1024 : 232448;
+  static constexpr int THREADS = 320;                 // 2 x 4 softmax warps, loads, products
+  static_assert(USED <= 232448, "shared memory");
+};
+
+struct PromptArgs {
+  const __nv_bfloat16 *Q, *K, *V;   // for rows beside values that are not finite
+  const int32_t *q_start, *kv_start;
+  __nv_bfloat16* O;
+  float* lse;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  int32_t n_seq, n_q, n_kv, h_q, h_kv, G, qt;
+  int32_t n_units;
+  float scale_log2;
+  uint32_t* err;
+};
+
+struct PromptUnit {
+  int q_row, q0, q_len, k_row, kv_len;   // first packed query row of the unit, its index in the sequence
+  bool any;
+};
+
+// Warp-collective.
+__device__ __forceinline__ PromptUnit prompt_unit(const PromptArgs& a, int unit) {
+  const int lane = threadIdx.x & 31, rows = 2 * a.qt;
+  PromptUnit u{};
+  const auto start = [&](int s) { return min(max(__ldg(a.q_start + s), 0), a.n_q); };
+  int lo = 0, hi = a.n_seq;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const bool le = s < hi && start(s) / rows + s <= unit;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    if (n == 0) return u;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int a0 = start(lo), a1 = max(start(lo + 1), a0);
+  const int64_t q0 = static_cast<int64_t>(unit - (a0 / rows + lo)) * rows;
+  if (q0 < 0 || q0 >= a1 - a0) return u;
+  u.k_row = min(max(__ldg(a.kv_start + lo), 0), a.n_kv);
+  u.kv_len = min(max(__ldg(a.kv_start + lo + 1), u.k_row), a.n_kv) - u.k_row;
+  u.q0 = static_cast<int>(q0);
+  u.q_row = a0 + u.q0;
+  u.q_len = a1 - a0;
+  u.any = true;
+  return u;
+}
+
+__device__ __forceinline__ uint64_t prompt_desc_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;   // next 64 dims
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;              // next 8 keys
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32"
+      " [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Packed pairs of float32.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// One row by a warp, without the tensor core: o of the row's own keys, from
+// its maximum reference (base-2) and sum.  For tiles where a value that some
+// rows do not attend is not finite (0 * inf is NaN in the product).
+template <int D>
+__device__ void plain_row(const PromptArgs& a, const __nv_bfloat16* q, const PromptUnit& u, int kvh, int pos, float m2,
+                          float inv_l, __nv_bfloat16* out) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  float x[E], o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    x[e] = __bfloat162float(q[lane * E + e]);
+    o[e] = 0.f;
+  }
+  for (int j = 0; j <= pos; ++j) {
+    const __nv_bfloat16* k = a.K + static_cast<int64_t>(u.k_row + j) * a.k_stride + kvh * D + lane * E;
+    const __nv_bfloat16* v = a.V + static_cast<int64_t>(u.k_row + j) * a.v_stride + kvh * D + lane * E;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(x[e], __bfloat162float(k[e]), s);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
+    const float p = fast_exp2(fmaf(s, a.scale_log2, -m2));
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(p, __bfloat162float(v[e]), o[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16(o[e] * inv_l);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PromptArgs a) {
+  using C = PromptShape<D>;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x % a.h_kv;
+  const PromptUnit u = prompt_unit(a, a.n_units - 1 - static_cast<int>(blockIdx.x / a.h_kv));
+  if (!u.any) return;   // the same for every warp
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (static_cast<int>(smem - smem_raw) + C::USED > C::SMEM) {   // never with a 1024-aligned base
+    if (threadIdx.x == 0) atomicCAS(a.err, 0u, static_cast<uint32_t>(SITE_PROMPT_SMEM));
+    return;
+  }
+  uint8_t* sQ = smem;                   // [2 tiles][halves][128 rows][128 B]
+  uint8_t* ring = smem + 2 * C::TILE;   // [slots][halves][128 keys][128 B]: K0 V0 K1 V1 ...
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
+  uint64_t* q_full = bars;
+  uint64_t* full = bars + 1;
+  uint64_t* empty = full + C::SLOTS;
+  uint64_t* s_full = empty + C::SLOTS;   // [2 tiles]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;         // the tile's last product is done
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+
+  // steps of each tile: keys 0 .. position of its last row
+  const int off = u.kv_len - u.q_len;
+  int steps[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int q_first = u.q0 + t * a.qt, q_last = min(q_first + a.qt, u.q_len) - 1;
+    steps[t] = q_first < u.q_len && q_last + off >= 0 ? (q_last + off) / 128 + 1 : 0;
+  }
+  const int n = max(steps[0], steps[1]);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[t], 4); mbar_init(&o_full[t], 1); }
+    mbar_init(mma_done, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;   // S of tile t at 128 t, O at 256 + 128 t
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && n > 0) {
+      uint32_t bytes = 0;
+      for (int t = 0; t < 2; ++t) bytes += steps[t] > 0 ? static_cast<uint32_t>(a.qt * a.G * C::ROW * C::HALVES) : 0;
+      mbar_arrive_expect_tx(q_full, bytes);
+      for (int t = 0; t < 2; ++t)
+        if (steps[t] > 0)
+#pragma unroll
+          for (int hf = 0; hf < C::HALVES; ++hf)
+            tma_load_3d(sQ + t * C::TILE + hf * 128 * C::ROW, &tmQ, q_full, hf * 64, kvh * a.G, u.q_row + t * a.qt);
+      int i = 0;
+      for (; i < 2 * n; ++i) {
+        const int slot = i % C::SLOTS, use = i / C::SLOTS;
+        if (use > 0 && !mbar_wait(&empty[slot], (use - 1) & 1, a.err, SITE_PROMPT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&full[slot], C::TILE);
+        const int row = u.k_row + (i / 2) * 128;
+#pragma unroll
+        for (int hf = 0; hf < C::HALVES; ++hf)
+          tma_load_3d(ring + slot * C::TILE + hf * 128 * C::ROW, (i & 1) ? &tmV : &tmK, &full[slot], hf * 64, kvh, row);
+      }
+      if (i < 2 * n) {   // a wait gave up: let the copies in flight land
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(q_full, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+        for (int k = max(0, i - C::SLOTS); k < i; ++k)
+          while (!mbar_try_wait(&full[k % C::SLOTS], (k / C::SLOTS) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 128);
+      constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);   // V is MN-major
+      const uint32_t sQ_u = smem_u32(sQ), ring_u = smem_u32(ring);
+      const auto wait_load = [&](int i) {
+        return mbar_wait(&full[i % C::SLOTS], (i / C::SLOTS) & 1, a.err, SITE_PROMPT_MMA);
+      };
+      const auto scores = [&](int t, int j) {   // S of tile t, step j (K is load 2 j)
+        const uint32_t k_u = ring_u + ((2 * j) % C::SLOTS) * C::TILE;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t at = (ks >> 2) * 128 * C::ROW + (ks & 3) * 32;
+          umma_bf16(tmem + 128 * t, umma_desc_sw128(sQ_u + t * C::TILE + at), umma_desc_sw128(k_u + at), IDESC_S,
+                    ks != 0);
+        }
+        umma_commit(&s_full[t]);
+      };
+      bool ok = n == 0 || (mbar_wait(q_full, 0, a.err, SITE_PROMPT_MMA) && wait_load(0));
+      if (ok && n > 0) {
+        for (int t = 0; t < 2; ++t)
+          if (steps[t] > 0) scores(t, 0);
+        umma_commit(&empty[0]);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const bool more = j + 1 < n;
+        ok = wait_load(2 * j + 1);
+        // the next keys come while the softmax works
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j < steps[t]) {
+            if (!mbar_wait(&p_full[t], j & 1, a.err, SITE_PROMPT_MMA)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t v_u = ring_u + ((2 * j + 1) % C::SLOTS) * C::TILE;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16_tmem_a(tmem + 256 + 128 * t, tmem + 128 * t + ks * 8,
+                               prompt_desc_mn(v_u + ks * 16 * C::ROW, 128 * C::ROW), IDESC_O, (j | ks) != 0);
+            if (j + 1 == steps[t]) umma_commit(&o_full[t]);
+          }
+          if (t == 1) umma_commit(&empty[(2 * j + 1) % C::SLOTS]);
+          // S over the P just read: products of one thread run in order
+          if (more && j + 1 < steps[t]) {
+            if (!wait_load(2 * j + 2)) { ok = false; break; }
+            scores(t, j + 1);
+          }
+          if (t == 1 && more) umma_commit(&empty[(2 * j + 2) % C::SLOTS]);
+        }
+      }
+      umma_commit(mma_done);   // all issued products complete before TMEM is freed
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(mma_done, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output, one row per thread
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + 128 * t, o_col = tmem + lanes + 256 + 128 * t;
+    const int qi = u.q0 + t * a.qt + row / a.G;             // query of the row within its sequence
+    const bool valid = row < a.qt * a.G && qi < u.q_len;
+    const int pos = valid ? qi + off : -1;
+    const int pos_first = u.q0 + t * a.qt + off;            // of the tile's first row
+    float m = -INFINITY;     // reference of the row, in logits before the scale
+    uint64_t l2[2] = {0, 0};
+    bool odd = false;        // a value that some rows do not attend is not finite
+    bool ok = true;
+    for (int j = 0; j < steps[t]; ++j) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[t], j & 1, a.err, SITE_PROMPT_SOFTMAX));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, r + 32 * c);
+      tmem_wait_ld();
+      tmem_regs_ready(r);
+      const bool masked = j * 128 + 127 > pos_first;        // the same for the tile
+      if (masked) {
+        const int last = pos - j * 128;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > last) r[c] = 0xFF800000u;
+      }
+      float mx[4] = {m, m, m, m};
+#pragma unroll
+      for (int c = 0; c < 128; c += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(r[c + 2 * k]), __uint_as_float(r[c + 2 * k + 1])));
+      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // a new reference only when the maximum has grown by 2^8 (or from nothing)
+      const bool grow = mn > m && (m == -INFINITY || (mn - m) * a.scale_log2 > 8.f);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float f = grow ? (m == -INFINITY ? 0.f : fast_exp2((m - mn) * a.scale_log2)) : 1.f;
+        if (grow) m = mn;
+        const uint64_t f2 = pair(f, f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) l2[k] = fma2(l2[k], f2, 0);
+        if (j > 0) {   // the tile's earlier products are done: this S came after them
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_col + 16 * c, o);
+            tmem_wait_ld();
+            tmem_regs_ready(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(o_col + 16 * c, o);
+          }
+        }
+      }
+      const float mr = m == -INFINITY ? 0.f : m;
+      const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), ms2 = pair(-mr * a.scale_log2, -mr * a.scale_log2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float x, y;
+          unpair(fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2), x, y);
+          x = fast_exp2(x);
+          y = fast_exp2(y);
+          l2[c & 1] = add2(l2[c & 1], pair(x, y));
+          p[c] = pack_bf16(x, y);
+        }
+        tmem_st32(s_col + 32 * h, p);
+      }
+      if (masked) {
+        // values of keys that some row of the tile does not attend: those
+        // behind the sequence become zero, those inside it are looked over
+        const int i = 2 * j + 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[i % C::SLOTS], (i / C::SLOTS) & 1, a.err, SITE_PROMPT_SOFTMAX));
+        if (!ok) break;
+        uint8_t* sV = ring + (i % C::SLOTS) * C::TILE;
+        const int end = min(u.kv_len - j * 128, 128), from = max(pos_first + 1 - j * 128, 0);
+        for (int x = row; x < (128 - from) * 8 * C::HALVES; x += 128) {
+          const int key = from + x / (8 * C::HALVES), c = x % (8 * C::HALVES);
+          uint4* w = reinterpret_cast<uint4*>(sV + (c >> 3) * 128 * C::ROW + key * C::ROW + (c & 7) * 16);
+          if (key >= end) {
+            *w = make_uint4(0, 0, 0, 0);
+          } else {
+            const uint4 v = *w;
+            odd |= not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    // whether any warp of the tile saw such a value (a barrier of its four warps)
+    int any_odd = 0;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(any_odd)
+        : "r"(odd ? 1 : 0), "r"(1 + t)
+        : "memory");
+    float l0, l1, l2_, l3;
+    unpair(l2[0], l0, l1);
+    unpair(l2[1], l2_, l3);
+    const float l = (l0 + l1) + (l2_ + l3);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float mr = m == -INFINITY ? 0.f : m * a.scale_log2;
+    const int head = kvh * a.G + row % a.G;
+    const int64_t q_row = u.q_row + t * a.qt + row / a.G;
+    __nv_bfloat16* out = a.O + q_row * a.o_stride + static_cast<int64_t>(head) * D;
+    if (ok && steps[t] > 0)
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], 0, a.err, SITE_PROMPT_SOFTMAX));
+    if (ok) {
+      if (valid && a.lse) a.lse[q_row * a.h_q + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
+      if (any_odd) {
+        const uint32_t vm = __ballot_sync(0xFFFFFFFFu, valid);
+        for (int k = 0; k < 32; ++k) {
+          if (!((vm >> k) & 1u)) continue;
+          const int64_t qr = __shfl_sync(0xFFFFFFFFu, q_row, k);
+          const int hd = __shfl_sync(0xFFFFFFFFu, head, k);
+          plain_row<D>(a, a.Q + qr * a.q_stride + static_cast<int64_t>(hd) * D, u, kvh,
+                       __shfl_sync(0xFFFFFFFFu, pos, k), __shfl_sync(0xFFFFFFFFu, mr, k),
+                       __shfl_sync(0xFFFFFFFFu, inv, k), a.O + qr * a.o_stride + static_cast<int64_t>(hd) * D);
+        }
+      } else {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (steps[t] > 0) {   // the same for the tile
+            tmem_ld32(o_col + 32 * c, o);
+            tmem_wait_ld();
+            tmem_regs_ready(o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          }
+          if (valid) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+              reinterpret_cast<uint4*>(out)[c * 4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t run_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PromptArgs& a,
+                       const LaunchCtx& c) {
+  using C = PromptShape<D>;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(a.n_units) * a.h_kv;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  prompt_kernel<D><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, c.stream>>>(tmQ, tmK, tmV, a);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const ssa_prompt_params& p, const void* Q, const void* K, const void* V,
+                               const int32_t* q_start, const int32_t* kv_start, void* O, float* lse,
+                               const LaunchCtx& c) {
+  PromptArgs a{};
+  a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.K = static_cast<const __nv_bfloat16*>(K);
+  a.V = static_cast<const __nv_bfloat16*>(V);
+  a.q_start = q_start; a.kv_start = kv_start;
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.lse = lse;
+  a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.v_stride = p.v_stride; a.o_stride = p.o_stride;
+  a.n_seq = p.n_seq; a.n_q = p.n_q; a.n_kv = p.n_kv; a.h_q = p.h_q; a.h_kv = p.h_kv;
+  a.G = p.h_q / p.h_kv;
+  a.qt = 128 / a.G;
+  a.n_units = p.n_q / (2 * a.qt) + p.n_seq;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.err = c.err;
+  // without key rows no unit loads any: the maps then describe the queries
+  CUtensorMap tmQ, tmK, tmV;
+  const bool kv = p.n_kv > 0;
+  if (!encode_heads(&tmQ, Q, p.d, p.h_q, p.n_q, p.q_stride, a.G, a.qt) ||
+      !encode_heads(&tmK, kv ? K : Q, p.d, kv ? p.h_kv : p.h_q, kv ? p.n_kv : p.n_q, kv ? p.k_stride : p.q_stride, 1,
+                    128) ||
+      !encode_heads(&tmV, kv ? V : Q, p.d, kv ? p.h_kv : p.h_q, kv ? p.n_kv : p.n_q, kv ? p.v_stride : p.q_stride, 1,
+                    128))
+    return cudaErrorInvalidValue;
+  return p.d == 128 ? run_prompt<128>(tmQ, tmK, tmV, a, c) : run_prompt<64>(tmQ, tmK, tmV, a, c);
+}
+
+}  // namespace ssa

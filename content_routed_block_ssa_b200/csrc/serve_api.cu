@@ -74,6 +74,23 @@ ssa_status check_cache_attn(const ssa_cache_attn_params* p) {
   return SSA_OK;
 }
 
+ssa_status check_prompt(const ssa_prompt_params* p) {
+  if (!p || p->n_seq < 0 || p->n_q < 0 || p->n_kv < 0 || p->h_q < 1 || p->h_kv < 1 || p->d < 1 || p->reserved != 0 ||
+      !isfinite(p->scale) || !(p->scale > 0.f) || p->h_q % p->h_kv != 0)
+    return SSA_ERR_INVALID_ARG;
+  if ((p->d != 64 && p->d != 128) || p->h_q / p->h_kv > 16) return SSA_ERR_UNSUPPORTED;
+  if (bad_stride(p->q_stride, p->h_q, p->d, 2) || bad_stride(p->k_stride, p->h_kv, p->d, 2) ||
+      bad_stride(p->v_stride, p->h_kv, p->d, 2) || bad_stride(p->o_stride, p->h_q, p->d, 2))
+    return SSA_ERR_INVALID_ARG;
+  // tensor-map strides are below 2^40 bytes; the grid is counted in 32 bits
+  const int64_t most = int64_t{1} << 38;
+  if (p->q_stride > most || p->k_stride > most || p->v_stride > most) return SSA_ERR_UNSUPPORTED;
+  if (p->n_seq > (1 << 24) || p->h_q > 65535 ||
+      (static_cast<int64_t>(p->n_q) + p->n_seq) * p->h_kv > INT32_MAX)
+    return SSA_ERR_UNSUPPORTED;
+  return SSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -175,6 +192,21 @@ ssa_status ssa_cache_attn(const ssa_cache_attn_params* pp, const void* Q, const 
   if ((st = ssa::make_launch_ctx(stream, c)) != SSA_OK) return st;
   const ssa::CacheAttnArgs a{Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale, block_idx, O, lse, bad_count, ws};
   return from_cuda(ssa::launch_cache_attn(p, a, c));
+}
+
+ssa_status ssa_prompt_attn(const ssa_prompt_params* pp, const void* Q, const void* K, const void* V,
+                           const int32_t* q_start, const int32_t* kv_start, void* O, float* lse, void* stream) {
+  ssa_status st = check_prompt(pp);
+  if (st != SSA_OK) return st;
+  const ssa_prompt_params& p = *pp;
+  if (p.n_seq == 0 || p.n_q == 0) return SSA_OK;
+  if (!Q || (p.n_kv > 0 && (!K || !V)) || !q_start || !kv_start || !O) return SSA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(q_start, 4) || !aligned(kv_start, 4) ||
+      !aligned(O, 16) || !aligned(lse, 4))
+    return SSA_ERR_INVALID_ARG;
+  LaunchCtx c;
+  if ((st = ssa::make_launch_ctx(stream, c)) != SSA_OK) return st;
+  return from_cuda(ssa::launch_prompt_attn(p, Q, K, V, q_start, kv_start, O, lse, c));
 }
 
 }  // extern "C"

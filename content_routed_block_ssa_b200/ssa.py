@@ -77,6 +77,15 @@ class ssa_cache_attn_params(C.Structure):
 assert C.sizeof(ssa_cache_attn_params) == 48
 
 
+class ssa_prompt_params(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("n_q", C.c_int32), ("n_kv", C.c_int32), ("h_q", C.c_int32),
+                ("h_kv", C.c_int32), ("d", C.c_int32), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("o_stride", C.c_int64), ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
+assert C.sizeof(ssa_prompt_params) == 64
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is missing: build it with "
@@ -114,6 +123,7 @@ def _load():
         "ssa_cache_append": (i32, [C.POINTER(ssa_append_params)] + [vp] * 13),
         "ssa_cache_attn_workspace_size": (sz, [C.POINTER(ssa_cache_attn_params)]),
         "ssa_cache_attn": (i32, [C.POINTER(ssa_cache_attn_params)] + [vp] * 12 + [sz, vp]),
+        "ssa_prompt_attn": (i32, [C.POINTER(ssa_prompt_params)] + [vp] * 8),
         "ssa_selftest_wait_timeout": (i32, [vp]),
     }
     for name, (res, args) in sig.items():
@@ -132,7 +142,7 @@ EXPORTED = ("ssa_status_string", "ssa_version", "ssa_launch_count", "ssa_device_
             "ssa_workspace_size", "ssa_forward", "ssa_hostio_buffer_size", "ssa_forward_hostio",
             "ssa_hier_nodes_size", "ssa_hier_nodes", "ssa_route_hier_workspace_size", "ssa_route_hier",
             "ssa_rope_frequencies", "ssa_qk_rope", "ssa_cache_append", "ssa_cache_attn_workspace_size",
-            "ssa_cache_attn",
+            "ssa_cache_attn", "ssa_prompt_attn",
             "ssa_selftest_wait_timeout")
 
 
@@ -479,6 +489,29 @@ def ssa_cache_attn(p, Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale,
                               _arg("O", O, q, torch.bfloat16), _arg("lse", lse, q[:3], torch.float32),
                               _arg("bad_count", bad_count, (1,), torch.int32), _ptr(ws), _nbytes(ws),
                               _stream(stream)), "ssa_cache_attn")
+
+
+def make_prompt_params(n_seq, n_q, n_kv, h_q, h_kv, d, q_stride=None, k_stride=None, v_stride=None, o_stride=None,
+                       scale=None) -> ssa_prompt_params:
+    """An ssa_prompt_params struct (strides None: dense; scale None: 1/sqrt(d))."""
+    return ssa_prompt_params(n_seq=n_seq, n_q=n_q, n_kv=n_kv, h_q=h_q, h_kv=h_kv, d=d,
+                             q_stride=h_q * d if q_stride is None else q_stride,
+                             k_stride=h_kv * d if k_stride is None else k_stride,
+                             v_stride=h_kv * d if v_stride is None else v_stride,
+                             o_stride=h_q * d if o_stride is None else o_stride,
+                             scale=(1.0 / math.sqrt(d)) if scale is None else scale)
+
+
+def ssa_prompt_attn(p, Q, K, V, q_start, kv_start, O, lse=None, stream=None):
+    """Causal attention over packed prompts of different lengths."""
+    q, kv = (p.n_q, p.h_q, p.d), (p.n_kv, p.h_kv, p.d)
+    _check(lib.ssa_prompt_attn(C.byref(p), _arg("Q", Q, q, torch.bfloat16, p.q_stride),
+                               _arg("K", K, kv, torch.bfloat16, p.k_stride),
+                               _arg("V", V, kv, torch.bfloat16, p.v_stride),
+                               _arg("q_start", q_start, (p.n_seq + 1,), torch.int32),
+                               _arg("kv_start", kv_start, (p.n_seq + 1,), torch.int32),
+                               _arg("O", O, q, torch.bfloat16, p.o_stride),
+                               _arg("lse", lse, q[:2], torch.float32), _stream(stream)), "ssa_prompt_attn")
 
 
 SITE_SELFTEST = 0x7F1

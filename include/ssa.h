@@ -605,6 +605,37 @@ SSA_API ssa_status ssa_cache_attn(const ssa_cache_attn_params* p, const void* Q,
                                   void* O, float* lse, int32_t* bad_count, void* ws, size_t ws_bytes,
                                   void* stream);
 
+/* 64 bytes, no padding. */
+typedef struct {
+  int32_t n_seq;
+  int32_t n_q, n_kv;  /* packed rows of Q and of K, V                           */
+  int32_t h_q, h_kv;  /* h_q / h_kv in 1..16                                    */
+  int32_t d;          /* 64 or 128                                              */
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  float scale;        /* logit scale, > 0                                       */
+  int32_t reserved;   /* 0                                                      */
+} ssa_prompt_params;
+
+/*
+ * Causal attention over packed prompts: sequence s has query rows
+ * q_start[s] .. q_start[s+1] - 1 and key rows kv_start[s] .. kv_start[s+1] - 1,
+ * its last query at its last key: row i attends keys 0 .. i + kv_len - q_len.
+ * A row without keys gives O = 0 and lse = -inf.  Rows of Q, K and V outside
+ * every sequence are not part of any result and their rows of O and lse stay
+ * as they were.  Keys that a row does not attend have no part in it,
+ * infinities and NaN among them.  Logits, softmax and sums are float32; the
+ * probabilities enter the second product as bf16.
+ *   Q          strided device [n_q, h_q, d] bf16
+ *   K, V       strided device [n_kv, h_kv, d] bf16
+ *   q_start, kv_start  device int32 [n_seq + 1], non-decreasing, within
+ *              0..n_q and 0..n_kv (may be one array)
+ *   O          strided device output [n_q, h_q, d] bf16
+ *   lse        device float32 output [n_q, h_q], may be NULL
+ */
+SSA_API ssa_status ssa_prompt_attn(const ssa_prompt_params* p, const void* Q, const void* K, const void* V,
+                                   const int32_t* q_start, const int32_t* kv_start, void* O, float* lse,
+                                   void* stream);
+
 /*
  * Self-test of the failure path (not part of the layer).  Launches on
  * `stream` one kernel that waits on an mbarrier nothing arrives at, through

@@ -13,6 +13,9 @@ Tolerances (half a unit in the last place u: bf16 2^-8, float32 2^-24, e4m3
     2^-25 absolute against the largest, so 2^-11 + n 2^-25 of sum p|v|/sum p
     with n <= 2^12 keys here), and 2^-11 is left for ex2.approx (2^-22) and
     float32 sums;
+  * packed prompts: u |o| for the output, u times the row's sum p|v| / sum p for
+    probabilities that enter the product as bf16, and 2^-12 of the largest |v|
+    for ex2.approx and float32 sums;
   * log-sum-exp: 2^-17 (1 + the largest sum |q_d k_d| scale): float32 sums of
     128 products and one exp2/log2 each way.
 """
@@ -490,6 +493,144 @@ def test_cache_attention_scales_and_queries_of_very_different_size():
     check_cache(o, lse, q * 0, lens, table, codes, scale, page)
 
 
+# ---------------------------------------------------------------- packed prompts
+
+def run_prompt(q, k, v, qs, ks, sm_scale=None, lse=True, stream=None):
+    T, h_q, d = q.shape
+    p = ssa.make_prompt_params(len(qs) - 1, T, k.shape[0], h_q, k.shape[1], d, q.stride(0), k.stride(0), v.stride(0),
+                               h_q * d + 8, sm_scale)
+    buf = torch.full((T, h_q * d + 8), 7.0, device="cuda", dtype=torch.bfloat16)   # strided, with a gap
+    o = buf[:, :h_q * d].view(T, h_q, d)
+    out_l = torch.full((T, h_q), 7.0, device="cuda") if lse else None
+    ssa.ssa_prompt_attn(p, q, k, v, dev(qs, torch.int32), dev(ks, torch.int32), o, out_l, stream)
+    ok()
+    assert (buf[:, h_q * d:] == 7.0).all()
+    return o, out_l
+
+
+def check_prompt(o, lse, q, k, v, qs, ks, sm_scale=None):
+    d = q.shape[-1]
+    sm = 1 / math.sqrt(d) if sm_scale is None else sm_scale
+    q, k, v, o, lse = f64(q), f64(k), f64(v), f64(o), f64(lse)
+    ro, rl = S.prompt_attention(q, k, v, qs, ks, sm)
+    ra, _ = S.prompt_attention(q, k, np.abs(v), qs, ks, sm)
+    out = np.isnan(ro)                                        # rows outside every sequence: as they were
+    assert (o[out] == 7.0).all() and (lse[np.isnan(rl)] == 7.0).all()
+    rows = ~out.any(-1)
+    vmax = max(np.abs(v[ks[0]:ks[-1]]).max(initial=0), 1e-30)
+    assert (np.abs(o - ro) <= 2.0 ** -8 * (np.abs(ro) + ra) + 2.0 ** -12 * vmax)[rows].all()
+    empty = rows & np.isinf(rl)
+    assert np.array_equal(np.isinf(lse) & rows, empty) and (o[empty] == 0).all()
+    rows &= ~empty
+    big = sm * np.abs(q).sum(-1).max(initial=0) * np.abs(k[ks[0]:ks[-1]]).max(initial=0)
+    assert (np.abs(lse[rows] - rl[rows]) <= 2.0 ** -17 * (1 + big)).all()
+
+
+def prompt_case(r, lens, kv_lens, h_kv, G, d, pad=3):
+    qs, ks = np.concatenate([[0], np.cumsum(lens)]), np.concatenate([[0], np.cumsum(kv_lens)])
+    T, N = int(qs[-1]) + pad, int(ks[-1]) + pad
+    x = dev(r.normal(size=(T, h_kv * G + 1, d)), torch.bfloat16)
+    y = dev(r.normal(size=(N, 2 * h_kv, d)) * r.choice([0.5, 1, 4], size=(N, 1, 1)), torch.bfloat16)
+    return x[:, :h_kv * G], y[:, :h_kv], y[:, h_kv:], qs, ks
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("h_kv,G", [(2, 4), (1, 8), (2, 1), (1, 3), (1, 16), (2, 2), (1, 7)])
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [127], [128, 129], [5, 0, 200, 1, 64], [300]])
+def test_prompt(d, h_kv, G, lens):
+    r = rng_of(d, h_kv, G, lens)
+    q, k, v, qs, ks = prompt_case(r, lens, lens, h_kv, G, d)
+    o, lse = run_prompt(q, k, v, qs, ks)
+    check_prompt(o, lse, q, k, v, qs, ks)
+
+
+@pytest.mark.parametrize("d,h_kv,G", [(128, 1, 4), (64, 2, 2)])
+@pytest.mark.parametrize("lens,kv_lens", [([1, 1, 1], [1, 128, 400]), ([40, 7], [300, 129]),       # keys before the prompt
+                                          ([50, 9, 300], [20, 0, 130]), ([3], [0]), ([200], [1])])  # rows without keys
+def test_prompt_with_other_key_lengths(d, h_kv, G, lens, kv_lens):
+    r = rng_of("kv", d, lens, kv_lens)
+    q, k, v, qs, ks = prompt_case(r, lens, kv_lens, h_kv, G, d)
+    o, lse = run_prompt(q, k, v, qs, ks)
+    check_prompt(o, lse, q, k, v, qs, ks)
+
+
+def test_prompt_large_logits_move_the_reference():
+    """Logits that grow along the keys by far more than the 2^8 at which the
+    running reference moves, and rows that one key dominates."""
+    r = rng_of("grow")
+    q, k, v, qs, ks = prompt_case(r, [700], [700], 1, 4, 128)
+    k *= torch.linspace(0.1, 20, k.shape[0], device="cuda", dtype=torch.bfloat16)[:, None, None]
+    o, lse = run_prompt(q, k, v, qs, ks, 1.0)
+    check_prompt(o, lse, q, k, v, qs, ks, 1.0)
+
+
+def test_prompt_ignores_what_a_row_does_not_attend():
+    """Infinities and NaN behind a sequence, in its neighbour or at later keys
+    have no part in a row; where a row attends them they show."""
+    r = rng_of("pnan")
+    lens = [150, 77, 260]
+    q, k, v, qs, ks = prompt_case(r, lens, lens, 1, 4, 128)
+    clean, clean_l = run_prompt(q, k, v, qs, ks)
+    k2, v2 = k.clone(), v.clone()
+    k2[ks[-1]:], v2[ks[-1]:] = math.nan, math.inf              # rows behind the last sequence
+    o, lse = run_prompt(q, k2, v2, qs, ks)
+    assert torch.equal(o, clean) and torch.equal(lse, clean_l)
+    bad = qs[1] + 40                                           # a value inside the second sequence
+    v2 = v.clone()
+    v2[bad, 0, 5], v2[bad + 1, 0, 9] = math.inf, math.nan
+    o, lse = run_prompt(q, k, v2, qs, ks)
+    assert torch.equal(lse, clean_l)
+    want = torch.zeros_like(o, dtype=torch.bool)
+    want[bad:qs[2], :, 5] = True
+    want[bad + 1:qs[2], :, 9] = True
+    want[qs[-1]:] = False
+    assert torch.equal(~torch.isfinite(o), want)
+    keep = ~want
+    keep[qs[1]:qs[2]] = False                                  # its own tile is evaluated another way
+    assert torch.equal(o[keep], clean[keep])
+    rows = slice(int(qs[1]), int(bad))
+    assert (o[rows].float() - clean[rows].float()).abs().max() <= 2.0 ** -6 * v.float().abs().max()
+    k2 = k.clone()
+    k2[bad, 0, 5] = math.nan                                   # a key: every later row of the sequence
+    o, lse = run_prompt(q, k2, v, qs, ks)
+    want = torch.zeros_like(lse, dtype=torch.bool)
+    want[bad:qs[2]] = True
+    assert torch.equal(lse.isnan(), want) and torch.equal(o.isnan(), want[..., None].expand_as(o))
+    assert torch.equal(o[~o.isnan()], clean[~o.isnan()])
+
+
+def test_prompt_offsets_that_do_not_fit():
+    """Decreasing or out-of-range offsets read and write nothing outside the
+    operands; rows that no sequence covers stay as they were."""
+    r = rng_of("poff")
+    q, k, v, qs, ks = prompt_case(r, [100, 100], [100, 100], 2, 4, 64, pad=0)
+    for odd in ([0, 1 << 30, -7], [-5, 300, 100], [200, 200, 200], [50, 20, 10]):
+        o, lse = run_prompt(q, k, v, odd, odd)
+    assert (o == 7.0).all() and (lse == 7.0).all()             # the last: no rows
+    o, lse = run_prompt(q, k, v, [0, 100, 300], [0, 100, 300])  # cut to what is there
+    check_prompt(o, lse, q, k, v, qs, ks)
+    o, _ = run_prompt(q, k, v, qs, ks, lse=False)
+    assert torch.equal(o, run_prompt(q, k, v, qs, ks)[0])
+
+
+@pytest.mark.parametrize("lens,h_kv,G,d", [([3000], 1, 8, 128), ([700, 1500, 33], 4, 4, 128), ([2049], 2, 2, 64)])
+def test_prompt_long(lens, h_kv, G, d):
+    """Many steps and more units than SMs, against float64 on sampled rows."""
+    r = rng_of("plong", lens)
+    q, k, v, qs, ks = prompt_case(r, lens, lens, h_kv, G, d, pad=0)
+    o, lse = run_prompt(q, k, v, qs, ks)
+    q, k, v, o, lse = map(f64, (q, k, v, o, lse))
+    for row in np.unique(np.concatenate([r.integers(0, len(o), 150), qs[1:] - 1, qs[:-1]])):
+        s = int(np.searchsorted(qs, row, side="right")) - 1
+        for h in range(h_kv * G):
+            a = (q[row, h], k[qs[s]:row + 1, h // G])
+            vv = v[qs[s]:row + 1, h // G]
+            ro, rl = S.attend(*a, vv, 1 / math.sqrt(d))
+            ra, _ = S.attend(*a, np.abs(vv), 1 / math.sqrt(d))
+            assert (np.abs(o[row, h] - ro) <= 2.0 ** -8 * (np.abs(ro) + ra) + 2.0 ** -12 * np.abs(vv).max()).all()
+            assert abs(lse[row, h] - rl) <= 2.0 ** -17 * (1 + np.abs(a[0]).sum() * np.abs(a[1]).max() / math.sqrt(d))
+
+
 # ---------------------------------------------------------------- together
 
 def test_a_serving_loop_matches_attention_over_everything():
@@ -582,6 +723,40 @@ def test_operators_run_on_a_side_stream_and_replay_from_a_graph():
     g.replay()
     ok()
     assert torch.equal(o, again)                                       # and the same bytes each time
+
+
+def test_prompt_then_decode_agree():
+    """The last row of a prompt equals a decode step over the cache that the
+    same prompt filled, when the codes hold the keys and values exactly; and the
+    prompt operator replays from a graph."""
+    r = rng_of("agree")
+    lens, h_kv, G, d, page = [200, 65], 2, 4, 64, 64
+    q, k, v, qs, ks = prompt_case(r, lens, lens, h_kv, G, d, pad=0)
+    val = S.e4m3_values()
+    k.copy_(dev(val[S.to_e4m3(f64(k) * 16)] / 16)), v.copy_(dev(val[S.to_e4m3(f64(v) * 16)] / 16))
+    o, lse = run_prompt(q, k, v, qs, ks)
+    table = np.arange(8).reshape(2, 4)
+    codes, scale = pool(r, 8, h_kv, page, d)
+    p = ssa.make_append_params(int(qs[-1]), 2, 4, 8, page, h_kv, d, 0, norm=False, k_stride=k.stride(0), v_stride=v.stride(0))
+    kc, vc, kss, vss = dev(codes[0]), dev(codes[1]), dev(scale[0], torch.float32), dev(scale[1], torch.float32)
+    ssa.ssa_cache_append(p, k, v, None, None, dev(qs, torch.int32), dev([0, 0], torch.int32), dev(table, torch.int32), kc, vc, kss, vss)
+    last = q[dev(qs[1:] - 1)].view(2, 1, h_kv * G, d).contiguous()
+    cs, sc = np.stack([kc.cpu().numpy(), vc.cpu().numpy()]), np.stack([f64(kss), f64(vss)])
+    o2, l2, _ = run_cache(last, lens, table, cs, sc, page)
+    at = dev(qs[1:] - 1)
+    assert (o2[:, 0].float() - o[at].float()).abs().max() <= 2.0 ** -6 * v.float().abs().max()
+    assert (l2[:, 0] - lse[at]).abs().max() <= 1e-3
+    pp = ssa.make_prompt_params(2, q.shape[0], k.shape[0], h_kv * G, h_kv, d, q.stride(0), k.stride(0), v.stride(0))
+    out, ol = torch.zeros(q.shape, device="cuda", dtype=torch.bfloat16), torch.zeros_like(lse)
+    st = dev(qs, torch.int32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ssa.ssa_prompt_attn(pp, q, k, v, st, st, out, ol)
+    for _ in range(2):
+        out.zero_(), ol.zero_()
+        g.replay()
+        ok()
+        assert torch.equal(out, o) and torch.equal(ol, lse)
 
 
 def test_results_do_not_depend_on_the_run():

@@ -16,7 +16,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 D = 256   # a non-null, 16-byte-aligned stand-in address: validation fails first
 
 
-@pytest.mark.parametrize("name", ["ssa_rope_params", "ssa_append_params", "ssa_cache_attn_params"])
+@pytest.mark.parametrize("name", ["ssa_rope_params", "ssa_append_params", "ssa_cache_attn_params", "ssa_prompt_params"])
 def test_struct_layouts_match_the_header(name):
     text = open(HEADER).read()
     body = text[:text.index("} %s;" % name)]
@@ -144,6 +144,42 @@ def test_cache_attn_pointers_and_workspace():
     assert call_cache(p) == INVALID
     assert call_cache(cache(n_seq=0), Q=None) == ssa.SSA_OK
     assert call_cache(cache(n_q=0), Q=None) == ssa.SSA_OK
+
+
+def prompt(**kw):
+    return ssa.make_prompt_params(**{**dict(n_seq=2, n_q=9, n_kv=9, h_q=8, h_kv=2, d=128), **kw})
+
+
+def call_prompt(p, **kw):
+    a = {**dict(Q=D, K=D, V=D, qs=D, ks=D, O=D, lse=None), **kw}
+    return ssa.lib.ssa_prompt_attn(C.byref(p), a["Q"], a["K"], a["V"], a["qs"], a["ks"], a["O"], a["lse"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_seq=-1), INVALID), (dict(n_q=-1), INVALID), (dict(n_kv=-1), INVALID), (dict(h_q=7), INVALID),
+    (dict(h_kv=0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(q_stride=1020), INVALID), (dict(k_stride=255), INVALID), (dict(v_stride=260), INVALID),
+    (dict(o_stride=512), INVALID), (dict(d=192), UNSUPPORTED), (dict(h_q=34), UNSUPPORTED),
+    (dict(q_stride=1 << 39), UNSUPPORTED),
+])
+def test_prompt_refusals(kw, code):
+    before = ssa.ssa_launch_count()
+    assert call_prompt(prompt(**kw)) == code
+    assert ssa.ssa_launch_count() == before
+
+
+def test_prompt_pointers():
+    p = prompt()
+    for n in ("Q", "K", "V", "qs", "ks", "O"):
+        assert call_prompt(p, **{n: None}) == INVALID, n
+    for n in ("Q", "K", "V", "O"):
+        assert call_prompt(p, **{n: D + 8}) == INVALID, n
+    for n in ("qs", "ks", "lse"):
+        assert call_prompt(p, **{n: D + 2}) == INVALID, n
+    p.reserved = 3
+    assert call_prompt(p) == INVALID
+    assert call_prompt(prompt(n_q=0), Q=None) == ssa.SSA_OK
+    assert call_prompt(prompt(n_seq=0), Q=None) == ssa.SSA_OK
 
 
 def test_binding_refuses_other_types_shapes_and_devices():

@@ -82,20 +82,25 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t un
   return u;
 }
 
+// The largest |x| of finite elements so far (fmaxf leaves NaN out).
 __device__ __forceinline__ float finite_amax(const float (&x)[8], float m) {
+  float r = m;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = fabsf(x[i]);
-    m = v <= 3.402823466e38f ? fmaxf(m, v) : m;   // infinities and NaN left out
+  for (int i = 0; i < 8; ++i) r = fmaxf(r, fabsf(x[i]));
+  if (r == INFINITY) {
+    r = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(x[i]) != INFINITY) r = fmaxf(r, fabsf(x[i]));
   }
-  return m;
+  return r;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[8], float inv) {
-  uint2 w;
-  w.x = to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
-  w.y = to_e4m3x2(x[4] * inv, x[5] * inv) | to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
-  *reinterpret_cast<uint2*>(p) = w;
+__device__ __forceinline__ void store_codes(uint8_t* row, const LaneDims& at, const float (&x)[8], float inv) {
+  *reinterpret_cast<uint32_t*>(row + at.a) =
+      to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+  *reinterpret_cast<uint32_t*>(row + at.b) =
+      to_e4m3x2(x[4] * inv, x[5] * inv) | to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
 }
 
 // Rounds 16 codes again to a scale 2^-down times coarser.
@@ -118,17 +123,21 @@ __device__ __forceinline__ void round_again(uint8_t* p, float down) {
 
 // One row's eight dims of this lane in float32: the key normed and rotated,
 // the value as it is.
-template <typename T, int LPR, bool PRECISE>
-__device__ __forceinline__ void append_row(const AppendCfg& a, bool is_k, const Row8<T>& r, const float (&w)[8],
-                                           const uint64_t (&phase)[8], int sub, int lane, int pos, float (&x)[8]) {
-  r.get(x);
-  if (!is_k) return;
-  if (a.norm) norm_row<LPR>(x, w, a.eps);
-  if (a.rot > 0) {
-    Turn<PRECISE> t;
-    t.set(phase, sub, a.rot, a.layout, pos, a.mscale);
-    t.apply(x, a.layout, lane, 8 * sub < a.rot);
+template <typename T, int LPR>
+__device__ __forceinline__ void append_row(const AppendCfg& a, bool is_k, const Row8<T>& r, const LaneDims& at,
+                                           const float (&w)[8], const uint64_t (&phase)[4], int pos, float (&y)[8]) {
+  if (!is_k) {
+    r.get(y);
+    return;
   }
+  float x[8];
+  r.get(x);
+  const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
+  Angles g;
+  g.set<sizeof(T) == 4>(at, phase, pos, a.mscale);
+  Turn t;
+  t.set(at, g, w);
+  t.apply(at, x, f, y);
 }
 
 // The page's exponent, and the rounding of what it held when that grows.
@@ -159,19 +168,20 @@ __global__ void __launch_bounds__(256) append_page_kernel(const AppendCfg a) {
   const T* src = is_k ? static_cast<const T*>(a.g.K) + static_cast<int64_t>(u.t0) * a.k_stride
                       : static_cast<const T*>(a.g.V) + static_cast<int64_t>(u.t0) * a.v_stride;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
-  src += static_cast<int64_t>(head) * D + 8 * sub;
+  src += static_cast<int64_t>(head) * D;
+  const LaneDims at(sub, is_k ? a.rot : 0, a.layout);
   Row8<T> r[KEEP];
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) r[k].load(src + static_cast<int64_t>(min(row + k * ROWS, u.n - 1)) * stride);
+  for (int k = 0; k < KEEP; ++k) r[k].load(src + static_cast<int64_t>(min(row + k * ROWS, u.n - 1)) * stride, at);
   float w[8];
-  uint64_t phase[8];
-  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, sub, w);
-  lane_phases(a.g.freq, sub, is_k ? a.rot : 0, a.layout, phase);
+  uint64_t phase[4];
+  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
+  at.phases(a.g.freq, sub, phase);
   float x[KEEP][8];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {   // rows past the last repeat it: the same maximum
-    append_row<T, LPR, sizeof(T) == 4>(a, is_k, r[k], w, phase, sub, lane, u.pos0 + min(row + k * ROWS, u.n - 1), x[k]);
+    append_row<T, LPR>(a, is_k, r[k], at, w, phase, u.pos0 + min(row + k * ROWS, u.n - 1), x[k]);
     amax = finite_amax(x[k], amax);
   }
 #pragma unroll
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(256) append_page_kernel(const AppendCfg a) {
   const float inv = pow2(-e);
 #pragma unroll
   for (int k = 0; k < KEEP; ++k)
-    if (row + k * ROWS < u.n) store_codes(codes + (u.slot0 + row + k * ROWS) * D + 8 * sub, x[k], inv);
+    if (row + k * ROWS < u.n) store_codes(codes + (u.slot0 + row + k * ROWS) * D, at, x[k], inv);
   __syncthreads();   // every thread has read the old scale
   if (threadIdx.x == 0) *scale = pow2(e);
 }
@@ -208,17 +218,18 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   if (u.page < 0) return;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const T* src = static_cast<const T*>(is_k ? a.g.K : a.g.V) + static_cast<int64_t>(u.t0) * stride +
-                 static_cast<int64_t>(head) * D + 8 * sub;
+                 static_cast<int64_t>(head) * D;
+  const LaneDims at(sub, is_k ? a.rot : 0, a.layout);
   float w[8];
-  uint64_t phase[8];
-  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, sub, w);
-  lane_phases(a.g.freq, sub, is_k ? a.rot : 0, a.layout, phase);
+  uint64_t phase[4];
+  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
+  at.phases(a.g.freq, sub, phase);
   float x[8];
   const auto value = [&](int i0) {
     const int i = min(i0 + row, u.n - 1);
     Row8<T> r;
-    r.load(src + static_cast<int64_t>(i) * stride);
-    append_row<T, LPR, sizeof(T) == 4>(a, is_k, r, w, phase, sub, lane, u.pos0 + i, x);
+    r.load(src + static_cast<int64_t>(i) * stride, at);
+    append_row<T, LPR>(a, is_k, r, at, w, phase, u.pos0 + i, x);
   };
   float amax = 0.f;
   for (int i0 = 0; i0 < u.n; i0 += RPW) {
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   const float inv = pow2(-e);
   for (int i0 = 0; i0 < u.n; i0 += RPW) {
     if (u.n > RPW) value(i0);
-    if (i0 + row < u.n) store_codes(codes + (u.slot0 + i0 + row) * D + 8 * sub, x, inv);
+    if (i0 + row < u.n) store_codes(codes + (u.slot0 + i0 + row) * D, at, x, inv);
   }
   __syncwarp();
   if (lane == 0) *scale = pow2(e);

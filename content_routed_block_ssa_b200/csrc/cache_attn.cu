@@ -2,20 +2,25 @@
 // selected blocks plus the window.
 //
 // A unit is up to 16 query rows that share a kv-head (new tokens x the G query
-// heads of the group; with selected blocks one token's G heads), the M = 16
-// rows of a warp's m16n8k16 products, and a unit's keys are cut into `splits`
-// runs, one block each, whose partial results a second kernel joins.  Each of
-// a block's four warps walks its own 32-key pieces (every fourth of the run)
-// with a ring of bulk copies of its own, so no warp waits for another until
-// the end.  The products are small against the bytes (2 G flops per byte):
-// this kernel is bound by reading codes, and what it does per code counts:
+// heads of the group; with selected blocks one token's G heads), and a unit's
+// keys are cut into `splits` runs, one block each, whose partial results a
+// second kernel joins.  Each of a block's four warps walks its own 32-key
+// pieces (every fourth of the run) with a ring of bulk copies of its own, so
+// no warp waits for another until the end.  The products are small against
+// the bytes (2 G flops per byte): the kernel is bound by reading codes, and
+// the instructions per code decide whether it keeps up:
 //
-//  * codes become float16 (exact) straight from shared memory to the B
+//  * the keys and the value dims are the M = 16 rows of the m16n8k16 products
+//    (S^T = K Q^T, O^T = V^T P^T) and the query rows their N = 8 columns: a
+//    group of up to eight rows wastes nothing, and a lane holds 8 logits and
+//    D/4 outputs.  P^T moves from the accumulator's layout to the operand's by
+//    one 8x8 transposition per eight keys.
+//  * codes become float16 (exact) straight from shared memory to the A
 //    operands, without a pass through float32.  The k index of a product may
 //    run over the dims (or keys) in any order as long as both operands agree,
-//    so a lane takes 16 consecutive bytes of a key (S) or of a value row (P V)
-//    and calls them its k indexes; for P V, bytes of two keys are paired by
-//    byte permutes before the conversion.
+//    so a lane takes 16 consecutive bytes of a key (S^T) or of a value row
+//    (O^T) and calls them its indexes; for O^T, bytes of two keys are paired
+//    by byte permutes before the conversion.
 //  * a page's key scale multiplies its logits; its value scale 2^e is added to
 //    the base-2 logits: P' = 2^(s + e - M), M the running maximum of s + e,
 //    is at most 1, fits float16 and needs no factor on the output, and the sum
@@ -35,6 +40,7 @@ namespace {
 
 constexpr int kPiece = 32;     // keys per piece
 constexpr int kWarps = 4;
+constexpr int kBlocks = 3;     // blocks per SM (2 with 16 rows a unit, by registers)
 constexpr int kMaxEnt = 32 + 4032 / 64 + 2;   // selected blocks and window blocks
 constexpr int kSmCount = 148;
 
@@ -42,6 +48,7 @@ struct CacheCfg {
   CacheAttnArgs g;
   int32_t n_seq, n_q, max_pages, n_pages, page, h_q, h_kv, G, topk, window;
   int32_t tiles;     // units per (sequence, kv-head)
+  int32_t unit_rows; // rows of a unit without selected blocks: 8 or 16
   int32_t rows;      // partial rows stored per unit
   int32_t splits;
   float scale_log2;
@@ -54,7 +61,7 @@ template <int D>
 struct CacheShape {
   static constexpr int K_BYTES = kPiece * D;
   static constexpr int STAGE = 2 * K_BYTES;
-  static constexpr int STAGES = 24576 / STAGE;
+  static constexpr int STAGES = 16384 / STAGE;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int OROW = D + 4;   // floats per row of the join, skewed over the banks
   static constexpr int BARS = kWarps * RING;
@@ -126,13 +133,14 @@ struct Piece {
   int page;      // -1: outside the pool
   int key0;      // position of its first key
   int lo;        // first position that counts (0, or the window's)
-  float ks, lvs, ivs;
+  float ks, vs;
 };
 
-template <int D, bool SEL>
-__global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheCfg a) {
+// R: query rows of a unit in groups of eight.
+template <int D, bool SEL, int R>
+__global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_kernel(const CacheCfg a) {
   using C = CacheShape<D>;
-  constexpr int NT = D / 8;     // output column tiles
+  constexpr int MT = D / 16;    // output tiles of 16 dims
   constexpr int VW = D / 32;    // words of a value row per lane
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
@@ -147,12 +155,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
   const int seq = unit / a.h_kv / a.tiles;
   const int len = min(max(__ldg(a.g.kv_len + seq), 0), a.max_pages * a.page);
   // rows of the unit: row r is token (r0 + r) / G, head (r0 + r) % G
-  const int r0 = SEL ? tile * a.G : tile * 16;
-  const int n_rows = SEL ? a.G : min(16, a.n_q * a.G - r0);
+  const int r0 = SEL ? tile * a.G : tile * 8 * R;
+  const int n_rows = SEL ? a.G : min(8 * R, a.n_q * a.G - r0);
   const int first = len - a.n_q;                                // position of token 0
   const int pos_lo = first + r0 / a.G, pos_hi = first + (r0 + n_rows - 1) / a.G;
-  const int pos_a = g < n_rows ? first + (r0 + g) / a.G : -1;   // rows g and g + 8 of this lane
-  const int pos_b = g + 8 < n_rows ? first + (r0 + g + 8) / a.G : -1;
+  int pos[R][2];   // of this lane's rows 8 n + 2 t and + 1
+#pragma unroll
+  for (int n = 0; n < R; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * n + 2 * t + c;
+      pos[n][c] = r < n_rows ? first + (r0 + r) / a.G : -1;
+    }
   const int ppb = a.page / kPiece;
   const int32_t* table = a.g.table + static_cast<int64_t>(seq) * a.max_pages;
   const int wlo = SEL ? max(pos_hi - a.window + 1, 0) : 0;
@@ -212,7 +226,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
     Piece p;
     p.page = -1;
     p.key0 = p.lo = 0;
-    p.ks = p.lvs = p.ivs = 0.f;
+    p.ks = p.vs = 0.f;
     if (i < n_my) {
       const int c = c0 + warp + i * kWarps;
       int blk = c / ppb;
@@ -227,9 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
         p.page = page;
         const int64_t ph = static_cast<int64_t>(page) * a.h_kv + kvh;
         p.ks = __ldg(a.g.ks + ph);
-        const float vs = fmaxf(__ldg(a.g.vs + ph), 1.17549435e-38f);
-        p.lvs = log2f(vs);
-        p.ivs = 1.f / vs;
+        p.vs = __ldg(a.g.vs + ph);
       } else if (a.g.bad) {
         atomicAdd(a.g.bad, 1);
       }
@@ -253,30 +265,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
     }
   };
 
-  Piece cur = fetch(lane), nxt = fetch(32 + lane);
+  Piece cur = fetch(lane);
 #pragma unroll
   for (int i = 0; i < C::STAGES; ++i)
     if (i < n_my) issue(i, cur);
+  Piece nxt = fetch(32 + lane);
 
-  // queries while the first copies fly
-  uint32_t qa[D / 64][8], qb[D / 64][8];
-  float fa, fb;
-  {
-    const auto row = [&](int r) {
-      const int R = r0 + r, i = R / a.G, h = R % a.G;
-      return static_cast<const __nv_bfloat16*>(a.g.Q) +
-             ((static_cast<int64_t>(seq) * a.n_q + i) * a.h_q + kvh * a.G + h) * D;
-    };
-    fa = load_query<D>(row(g < n_rows ? g : 0), t, g < n_rows, a.scale_log2, qa);
-    fb = load_query<D>(row(g + 8 < n_rows ? g + 8 : 0), t, g + 8 < n_rows, a.scale_log2, qb);
+  // queries while the first copies fly: the B operand of row 8 n + g
+  uint32_t Q[R][D / 64][8];
+  float qf[R][2];   // logit factors of this lane's rows
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    const int r = 8 * n + g;
+    const int row = r0 + (r < n_rows ? r : 0), i = row / a.G, h = row % a.G;
+    const float f = load_query<D>(static_cast<const __nv_bfloat16*>(a.g.Q) +
+                                      ((static_cast<int64_t>(seq) * a.n_q + i) * a.h_q + kvh * a.G + h) * D,
+                                  t, r < n_rows, a.scale_log2, Q[n]);
+    qf[n][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+    qf[n][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
   }
 
-  float O[NT][4];
+  // O[n][j]: dims D/8 g + 2 j (c = 0, 1) and + 1 (c = 2, 3), rows 8 n + 2 t (c even) and + 1
+  float O[R][MT][4];
+  float M[R][2], l[R][2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int n = 0; n < R; ++n) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) O[j][c] = 0.f;
-  float Ma = -INFINITY, Mb = -INFINITY, la = 0.f, lb = 0.f;
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) O[n][j][c] = 0.f;
+    M[n][0] = M[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+  }
 
   int done = 0;
   for (; done < n_my; ++done) {
@@ -288,90 +308,104 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
     const int page = __shfl_sync(0xFFFFFFFFu, cur.page, b);
     const int key0 = __shfl_sync(0xFFFFFFFFu, cur.key0, b);
     const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, b);
-    const float lvs = __shfl_sync(0xFFFFFFFFu, cur.lvs, b);
-    const float ivs = __shfl_sync(0xFFFFFFFFu, cur.ivs, b);
+    const float vs = fmaxf(__shfl_sync(0xFFFFFFFFu, cur.vs, b), 1.17549435e-38f);
     const int lo = SEL ? __shfl_sync(0xFFFFFFFFu, cur.lo, b) : 0;
     const int st = i % C::STAGES;
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::STAGES) & 1, a.err, SITE_CACHE_FULL))) break;
     if (page >= 0) {
       const uint8_t* sK = ring + st * C::STAGE;
       const uint8_t* sV = sK + C::K_BYTES;
+      const float lvs = log2f(vs), ivs = 1.f / vs;
       const bool partial = key0 + kPiece - 1 > pos_lo || key0 < lo;
-      // S = Q K^T: key tile nt holds keys nt*8 .. nt*8+7, this lane's key nt*8+g
-      float S[4][4];
+      // S^T = K Q^T: keys 16 q + g (c = 0, 1) and + 8 (c = 2, 3) of this lane
+      float S[R][2][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) S[nt][c] = 0.f;
+        for (int n = 0; n < R; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) S[n][q][c] = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint4 kv = *reinterpret_cast<const uint4*>(sK + (nt * 8 + g) * D + c * 64 + t * 16);
-          const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+          const uint4 x = *reinterpret_cast<const uint4*>(sK + (q * 16 + g) * D + c * 64 + t * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(sK + (q * 16 + 8 + g) * D + c * 64 + t * 16);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const uint32_t A[4] = {qa[c][2 * s], qb[c][2 * s], qa[c][2 * s + 1], qb[c][2 * s + 1]};
-            mma_f16(S[nt], A, e4m3x2_to_half2(w[s] & 0xFFFFu), e4m3x2_to_half2(w[s] >> 16));
+            uint32_t A[4];
+            e4m3x4_to_half2(xw[s], A[0], A[2]);
+            e4m3x4_to_half2(yw[s], A[1], A[3]);
+#pragma unroll
+            for (int n = 0; n < R; ++n) mma_f16(S[n][q], A, Q[n][c][2 * s], Q[n][c][2 * s + 1]);
           }
         }
       }
-      const float ka = fa * ks, kb = fb * ks;
-      float ma = -INFINITY, mb = -INFINITY;
+      float m[R][2];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int n = 0; n < R; ++n) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          S[nt][c] = fmaf(S[nt][c], ka, lvs);
-          S[nt][2 + c] = fmaf(S[nt][2 + c], kb, lvs);
-          if (partial) {
-            const int kp = key0 + nt * 8 + 2 * t + c;
-            if (kp > pos_a || kp < lo) S[nt][c] = -INFINITY;
-            if (kp > pos_b || kp < lo) S[nt][2 + c] = -INFINITY;
+          const float f = qf[n][c] * ks;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            S[n][q][c] = fmaf(S[n][q][c], f, lvs);
+            S[n][q][2 + c] = fmaf(S[n][q][2 + c], f, lvs);
+            if (partial) {
+              const int kp = key0 + q * 16 + g;
+              if (kp > pos[n][c] || kp < lo) S[n][q][c] = -INFINITY;
+              if (kp + 8 > pos[n][c] || kp + 8 < lo) S[n][q][2 + c] = -INFINITY;
+            }
           }
-          ma = fmaxf(ma, S[nt][c]);
-          mb = fmaxf(mb, S[nt][2 + c]);
+          m[n][c] = fmaxf(fmaxf(S[n][0][c], S[n][0][2 + c]), fmaxf(S[n][1][c], S[n][1][2 + c]));
         }
       }
-      ma = fmaxf(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 1));
-      mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 1));
-      ma = fmaxf(ma, __shfl_xor_sync(0xFFFFFFFFu, ma, 2));
-      mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, 2));
-      if (__any_sync(0xFFFFFFFFu, ma > Ma || mb > Mb)) {   // a maximum moved: rescale
-        const float na = fmaxf(Ma, ma), nb = fmaxf(Mb, mb);
-        const float xa = na == -INFINITY ? 1.f : fast_exp2(Ma - na), xb = nb == -INFINITY ? 1.f : fast_exp2(Mb - nb);
-        Ma = na;
-        Mb = nb;
-        la *= xa;
-        lb *= xb;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          O[j][0] *= xa;
-          O[j][1] *= xa;
-          O[j][2] *= xb;
-          O[j][3] *= xb;
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) m[n][c] = fmaxf(m[n][c], __shfl_xor_sync(0xFFFFFFFFu, m[n][c], o));
+      bool moved = false;
+#pragma unroll
+      for (int n = 0; n < R; ++n) moved = moved || m[n][0] > M[n][0] || m[n][1] > M[n][1];
+      if (__any_sync(0xFFFFFFFFu, moved)) {   // a maximum moved: rescale
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+          float x[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float to = fmaxf(M[n][c], m[n][c]);
+            x[c] = to == -INFINITY ? 1.f : fast_exp2(M[n][c] - to);
+            M[n][c] = to;
+            l[n][c] *= x[c];
+          }
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) O[n][j][c] *= x[c & 1];
         }
       }
-      const float ra = Ma == -INFINITY ? 0.f : Ma, rb = Mb == -INFINITY ? 0.f : Mb;
-      float sa = 0.f, sb = 0.f;
+      uint32_t P[R][2][2];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int n = 0; n < R; ++n) {
+        const float ra = M[n][0] == -INFINITY ? 0.f : M[n][0], rb = M[n][1] == -INFINITY ? 0.f : M[n][1];
+        float sa = 0.f, sb = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          S[nt][c] = fast_exp2(S[nt][c] - ra);
-          S[nt][2 + c] = fast_exp2(S[nt][2 + c] - rb);
-          sa += S[nt][c];
-          sb += S[nt][2 + c];
-        }
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float x = fast_exp2(S[n][q][2 * k] - ra), y = fast_exp2(S[n][q][2 * k + 1] - rb);
+            sa += x;
+            sb += y;
+            P[n][q][k] = movmatrix_trans(half2_bits(x, y));   // keys 16 q + 8 k + 2 t, + 1 of row 8 n + g
+          }
+        l[n][0] = fmaf(sa, ivs, l[n][0]);
+        l[n][1] = fmaf(sb, ivs, l[n][1]);
       }
-      la = fmaf(sa, ivs, la);
-      lb = fmaf(sb, ivs, lb);
-      // O += P V: keys 16 q + {2t, 2t+1, 2t+8, 2t+9}, this lane's output
-      // columns NT g + j
+      // O^T += V^T P^T: keys 16 q + {2t, 2t+1, 2t+8, 2t+9}
       uint32_t odd = 0;   // NaN among values that not every row attends
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const uint32_t A[4] = {half2_bits(S[2 * q][0], S[2 * q][1]), half2_bits(S[2 * q][2], S[2 * q][3]),
-                               half2_bits(S[2 * q + 1][0], S[2 * q + 1][1]),
-                               half2_bits(S[2 * q + 1][2], S[2 * q + 1][3])};
         uint32_t v[4][VW];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -390,22 +424,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
               if (kp > pos_hi || kp < lo) {
                 v[k][w] = 0;   // no row attends it
               } else {
-                const uint32_t n = nan_bytes(v[k][w]);
-                odd |= n;
-                v[k][w] &= ~((n >> 7) * 0xFFu);
+                const uint32_t nb = nan_bytes(v[k][w]);
+                odd |= nb;
+                v[k][w] &= ~((nb >> 7) * 0xFFu);
               }
             }
           }
         }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          const uint32_t e0 = __byte_perm(v[0][w], v[1][w], 0x5140), e1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t o0 = __byte_perm(v[2][w], v[3][w], 0x5140), o1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-          mma_f16(O[4 * w + 0], A, e4m3x2_to_half2(e0 & 0xFFFFu), e4m3x2_to_half2(o0 & 0xFFFFu));
-          mma_f16(O[4 * w + 1], A, e4m3x2_to_half2(e0 >> 16), e4m3x2_to_half2(o0 >> 16));
-          mma_f16(O[4 * w + 2], A, e4m3x2_to_half2(e1 & 0xFFFFu), e4m3x2_to_half2(o1 & 0xFFFFu));
-          mma_f16(O[4 * w + 3], A, e4m3x2_to_half2(e1 >> 16), e4m3x2_to_half2(o1 >> 16));
-        }
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x7362 : 0x5140;
+            uint32_t A[4];
+            e4m3x4_to_half2(__byte_perm(v[0][w], v[1][w], sel), A[0], A[1]);
+            e4m3x4_to_half2(__byte_perm(v[2][w], v[3][w], sel), A[2], A[3]);
+#pragma unroll
+            for (int n = 0; n < R; ++n) mma_f16(O[n][2 * w + h], A, P[n][q][0], P[n][q][1]);
+          }
       }
       if (partial && __any_sync(0xFFFFFFFFu, odd != 0)) {
         // 0 * NaN is NaN: such values stay out of the product and reach the
@@ -415,12 +451,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
           const int kp = key0 + key;
           if (kp > pos_hi || kp < lo) continue;
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if ((sV[key * D + (2 * t + c) * NT + j] & 0x7F) == 0x7F) {
-                if (kp <= pos_a) O[j][c] = bad;
-                if (kp <= pos_b) O[j][2 + c] = bad;
+            for (int c = 0; c < 4; ++c)
+              if ((sV[key * D + g * (D / 8) + 2 * j + (c >> 1)] & 0x7F) == 0x7F) {
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                  if (kp <= pos[n][c & 1]) O[n][j][c] = bad;
               }
         }
       }
@@ -442,102 +479,123 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_attn_kernel(const CacheC
   }
 
   // join the four warps: maxima and sums, then outputs, through the rings
-  la += __shfl_xor_sync(0xFFFFFFFFu, la, 1);
-  lb += __shfl_xor_sync(0xFFFFFFFFu, lb, 1);
-  la += __shfl_xor_sync(0xFFFFFFFFu, la, 2);
-  lb += __shfl_xor_sync(0xFFFFFFFFu, lb, 2);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int n = 0; n < R; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], o);
   __syncthreads();
-  float* jo = reinterpret_cast<float*>(smem);                                     // [warps][16][OROW]
-  float2* jml = reinterpret_cast<float2*>(jo + kWarps * 16 * C::OROW);            // [warps][16]
-  if (t == 0) {
-    jml[warp * 16 + g] = make_float2(Ma, la);
-    jml[warp * 16 + g + 8] = make_float2(Mb, lb);
-  }
-  {
-    float* ra = jo + (warp * 16 + g) * C::OROW + 2 * t * NT;
-    float* rb = ra + 8 * C::OROW;
-    const bool wa = g < n_rows, wb = g + 8 < n_rows;
+  float* jo = reinterpret_cast<float*>(smem);                                // [warps][8 R][OROW]
+  float2* jml = reinterpret_cast<float2*>(jo + kWarps * 8 * R * C::OROW);    // [warps][8 R]
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+  for (int n = 0; n < R; ++n)
 #pragma unroll
-      for (int j = 0; j < NT; j += 4) {
-        if (wa) *reinterpret_cast<float4*>(ra + c * NT + j) = make_float4(O[j][c], O[j + 1][c], O[j + 2][c], O[j + 3][c]);
-        if (wb)
-          *reinterpret_cast<float4*>(rb + c * NT + j) =
-              make_float4(O[j][2 + c], O[j + 1][2 + c], O[j + 2][2 + c], O[j + 3][2 + c]);
+    for (int c = 0; c < 2; ++c) {
+      const int r = 8 * n + 2 * t + c;
+      if (g == 0) jml[warp * 8 * R + r] = make_float2(M[n][c], l[n][c]);
+      if (r < n_rows) {
+        float* to = jo + (warp * 8 * R + r) * C::OROW + g * (D / 8);
+#pragma unroll
+        for (int j = 0; j < MT; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) =
+              make_float4(O[n][j][c], O[n][j][2 + c], O[n][j + 1][c], O[n][j + 1][2 + c]);
       }
-  }
+    }
   __syncthreads();
   constexpr int QR = D / 4;   // threads per row
   for (int x = threadIdx.x; x < n_rows * QR; x += kWarps * 32) {
     const int r = x / QR, q = x % QR;
-    float M = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, jml[w * 16 + r].x);
-    float l = 0.f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, jml[w * 8 * R + r].x);
+    float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = jml[w * 16 + r];
-      const float f = M == -INFINITY ? 1.f : exp2f(ml.x - M);
-      const float4 y = *reinterpret_cast<const float4*>(jo + (w * 16 + r) * C::OROW + 4 * q);
-      l = fmaf(f, ml.y, l);
+      const float2 ml = jml[w * 8 * R + r];
+      const float f = top == -INFINITY ? 1.f : exp2f(ml.x - top);
+      const float4 y = *reinterpret_cast<const float4*>(jo + (w * 8 * R + r) * C::OROW + 4 * q);
+      sum = fmaf(f, ml.y, sum);
       o.x = fmaf(f, y.x, o.x); o.y = fmaf(f, y.y, o.y); o.z = fmaf(f, y.z, o.z); o.w = fmaf(f, y.w, o.w);
     }
     if (a.splits > 1) {
       const int64_t pr = (static_cast<int64_t>(unit) * a.splits + split) * a.rows + r;
       reinterpret_cast<float4*>(a.part_o + pr * D)[q] = o;
-      if (q == 0) a.part_ml[pr] = make_float2(M, l);
+      if (q == 0) a.part_ml[pr] = make_float2(top, sum);
     } else {
-      const int R = r0 + r;
-      const int64_t row = (static_cast<int64_t>(seq) * a.n_q + R / a.G) * a.h_q + kvh * a.G + R % a.G;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int at = r0 + r;
+      const int64_t row = (static_cast<int64_t>(seq) * a.n_q + at / a.G) * a.h_q + kvh * a.G + at % a.G;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       uint2 out;
       out.x = pack_bf16(o.x * inv, o.y * inv);
       out.y = pack_bf16(o.z * inv, o.w * inv);
       reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.g.O) + row * D)[q] = out;
-      if (q == 0 && a.g.lse) a.g.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+      if (q == 0 && a.g.lse) a.g.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
 }
 
-// Joins the splits of every row: one warp per row.
+// Joins the splits of every row: `warps` warps per row (1, 2, 4 or 8, by the
+// number of splits), each every warps-th split.
 template <int D, bool SEL>
-__global__ void __launch_bounds__(128) cache_join_kernel(const CacheCfg a) {
+__global__ void __launch_bounds__(256) cache_join_kernel(const CacheCfg a, const int warps) {
   constexpr int E = D / 32;   // dims per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+  __shared__ float so[8][D];
+  __shared__ float2 sml[8];
+  // launched while the split kernel still runs: its results are complete after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, w = warp % warps;
+  const int64_t item = (static_cast<int64_t>(blockIdx.x) * 8 + warp) / warps;
   const int64_t unit = item / a.rows;
   const int r = static_cast<int>(item % a.rows);
-  if (unit >= static_cast<int64_t>(a.n_seq) * a.tiles * a.h_kv) return;
   const int kvh = static_cast<int>(unit % a.h_kv);
   const int tile = static_cast<int>(unit / a.h_kv % a.tiles);
-  const int seq = static_cast<int>(unit / a.h_kv / a.tiles);
-  const int R = (SEL ? tile * a.G : tile * 16) + r;
-  if (R >= a.n_q * a.G) return;
-  const float2* ml = a.part_ml + unit * a.splits * a.rows + r;
-  const float* po = a.part_o + (unit * a.splits * a.rows + r) * D + lane * E;
-  float M = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, ml[static_cast<int64_t>(s) * a.rows].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float l = 0.f, acc[E];
+  const int64_t seq = unit / a.h_kv / a.tiles;
+  const int at = (SEL ? tile * a.G : tile * a.unit_rows) + r;
+  const bool valid = seq < a.n_seq && at < a.n_q * a.G;
+  float M = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 x = ml[static_cast<int64_t>(s) * a.rows];
-    const float f = M == -INFINITY ? 1.f : exp2f(x.x - M);
-    const float* y = po + static_cast<int64_t>(s) * a.rows * D;
-    l = fmaf(f, x.y, l);
+  if (valid) {
+    const float2* ml = a.part_ml + unit * a.splits * a.rows + r;
+    const float* po = a.part_o + (unit * a.splits * a.rows + r) * D + lane * E;
+    for (int s = w + warps * lane; s < a.splits; s += 32 * warps) M = fmaxf(M, ml[static_cast<int64_t>(s) * a.rows].x);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(y + e);
-      acc[e] = fmaf(f, v.x, acc[e]);
-      acc[e + 1] = fmaf(f, v.y, acc[e + 1]);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+#pragma unroll 4
+    for (int s = w; s < a.splits; s += warps) {
+      const float2 x = ml[static_cast<int64_t>(s) * a.rows];
+      const float f = M == -INFINITY ? 1.f : exp2f(x.x - M);
+      const float* y = po + static_cast<int64_t>(s) * a.rows * D;
+      l = fmaf(f, x.y, l);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(y + e);
+        acc[e] = fmaf(f, v.x, acc[e]);
+        acc[e + 1] = fmaf(f, v.y, acc[e + 1]);
+      }
     }
   }
-  const int64_t row = (static_cast<int64_t>(seq) * a.n_q + R / a.G) * a.h_q + kvh * a.G + R % a.G;
+  if (warps > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) sml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (w != 0) return;
+    for (int k = 1; k < warps; ++k) M = fmaxf(M, sml[warp + k].x);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k = 0; k < warps; ++k) {
+      const float f = M == -INFINITY ? 1.f : exp2f(sml[warp + k].x - M);
+      l = fmaf(f, sml[warp + k].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, so[warp + k][lane * E + e], acc[e]);
+    }
+  }
+  if (!valid) return;
+  const int64_t row = (seq * a.n_q + at / a.G) * a.h_q + kvh * a.G + at % a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.g.O) + row * D + lane * E);
 #pragma unroll
@@ -547,43 +605,64 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheCfg a) {
 
 struct Split {
   int64_t units;
-  int tiles, rows, splits;
+  int tiles, unit_rows, rows, splits;
 };
 
 Split split_of(const ssa_cache_attn_params& p) {
   Split s;
   const int G = p.h_q / p.h_kv;
   const bool sel = p.topk > 0;
-  s.tiles = sel ? p.n_q : (p.n_q * G + 15) / 16;
-  s.rows = sel ? G : (p.n_q * G < 16 ? p.n_q * G : 16);
+  s.unit_rows = (sel ? G : p.n_q * G) <= 8 ? 8 : 16;
+  s.tiles = sel ? p.n_q : (p.n_q * G + s.unit_rows - 1) / s.unit_rows;
+  s.rows = sel ? G : (p.n_q * G < s.unit_rows ? p.n_q * G : s.unit_rows);
   s.units = static_cast<int64_t>(p.n_seq) * p.h_kv * s.tiles;
   int64_t pieces = static_cast<int64_t>(p.max_pages) * p.page / kPiece;
   if (sel) {
     const int64_t most = (p.topk + p.window / p.page + 2) * static_cast<int64_t>(p.page / kPiece);
     if (pieces > most) pieces = most;
   }
-  // two blocks per SM run at a time: one wave of them when the units are
+  // kBlocks blocks per SM run at a time: one wave of them when the units are
   // fewer, else about three, so that ragged lengths even out; at least four
   // pieces per warp
-  const int64_t room = 2 * kSmCount;
+  const int64_t room = kBlocks * kSmCount;
   int64_t n = s.units < 1 ? 1 : s.units < room ? room / s.units : (3 * room + s.units - 1) / s.units;
   if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
   s.splits = static_cast<int>(n < 1 ? 1 : n);
   return s;
 }
 
-template <int D, bool SEL>
+template <int D, bool SEL, int R>
 cudaError_t run_cache_attn(const CacheCfg& a, int64_t units, const LaunchCtx& c) {
   using C = CacheShape<D>;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e =
+      cudaFuncSetAttribute(cache_attn_kernel<D, SEL, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   if (units * a.splits > INT32_MAX) return cudaErrorInvalidValue;
-  cache_attn_kernel<D, SEL><<<static_cast<unsigned>(units * a.splits), kWarps * 32, C::SMEM, c.stream>>>(a);
+  cache_attn_kernel<D, SEL, R><<<static_cast<unsigned>(units * a.splits), kWarps * 32, C::SMEM, c.stream>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-  cache_join_kernel<D, SEL><<<static_cast<unsigned>((units * a.rows + 3) / 4), 128, 0, c.stream>>>(a);
+  int warps = 1;
+  while (warps < 8 && warps * 4 < a.splits) warps *= 2;
+  // its launch overlaps the end of the split kernel (it waits for it itself)
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((units * a.rows * warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = c.stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, cache_join_kernel<D, SEL>, a, warps);
   note_launch();
-  return cudaGetLastError();
+  return e;
+}
+
+template <int D>
+cudaError_t pick_cache_attn(const CacheCfg& a, int64_t units, const LaunchCtx& c) {
+  if (a.topk)
+    return a.unit_rows == 8 ? run_cache_attn<D, true, 1>(a, units, c) : run_cache_attn<D, true, 2>(a, units, c);
+  return a.unit_rows == 8 ? run_cache_attn<D, false, 1>(a, units, c) : run_cache_attn<D, false, 2>(a, units, c);
 }
 
 }  // namespace
@@ -600,14 +679,12 @@ cudaError_t launch_cache_attn(const ssa_cache_attn_params& p, const CacheAttnArg
   a.g = g;
   a.n_seq = p.n_seq; a.n_q = p.n_q; a.max_pages = p.max_pages; a.n_pages = p.n_pages; a.page = p.page;
   a.h_q = p.h_q; a.h_kv = p.h_kv; a.G = p.h_q / p.h_kv; a.topk = p.topk; a.window = p.window;
-  a.tiles = s.tiles; a.rows = s.rows; a.splits = s.splits;
+  a.tiles = s.tiles; a.unit_rows = s.unit_rows; a.rows = s.rows; a.splits = s.splits;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.part_o = static_cast<float*>(g.ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(s.units) * s.splits * s.rows * p.d);
   a.err = c.err;
-  if (p.d == 128)
-    return p.topk ? run_cache_attn<128, true>(a, s.units, c) : run_cache_attn<128, false>(a, s.units, c);
-  return p.topk ? run_cache_attn<64, true>(a, s.units, c) : run_cache_attn<64, false>(a, s.units, c);
+  return p.d == 128 ? pick_cache_attn<128>(a, s.units, c) : pick_cache_attn<64>(a, s.units, c);
 }
 
 }  // namespace ssa

@@ -2,10 +2,11 @@
 // (rope.cuh has the mathematics).
 //
 // A warp takes one token and a run of its heads (queries, then keys): 32/LPR
-// heads at a time, LPR = d/8 lanes of eight dims each, so a head is read and
-// written in 16-byte pieces and its norm is a few shuffles.  The angles of a
-// token are computed once per lane and used for all the heads of the run.
-// Bytes bound it: each element is read once and written once.
+// heads at a time, LPR = d/8 lanes of eight dims each, so that a head is read
+// and written whole and its norm is a few shuffles.  The angles of a token are
+// computed once per lane, folded with the weights, and used for all the heads
+// of the run; with many tokens a warp goes on to the next token and keeps its
+// frequencies.  Bytes bound it: each element is read once and written once.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -26,63 +27,61 @@ struct RopeArgs {
   float eps, mscale;
 };
 
+// The heads g * RPW + hr, g in [g0, g1), of one of the two operands.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes per head, heads per warp
-  constexpr int U = 4;                         // head groups in flight
-  constexpr bool PRECISE = sizeof(T) == 4;
-  const int lane = threadIdx.x & 31, sub = lane % LPR, hr = lane / LPR;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
-  const int64_t token = item / a.runs;
-  if (token >= a.n_tokens) return;
-  const int run = static_cast<int>(item % a.runs);
-  const int heads = a.h_q + a.h_kv;
-  const int h_end = min(heads, (run + 1) * a.per_run * RPW);
-
-  uint64_t phase[8];
-  Turn<PRECISE> turn;
-  lane_phases(a.freq, sub, a.rot, a.layout, phase);
-  turn.set(phase, sub, a.rot, a.layout, a.rot > 0 ? __ldg(a.pos + token) : 0, a.mscale);
-  float qw[8], kw[8];
-  lane_weights(a.qw, sub, qw);
-  lane_weights(a.kw, sub, kw);
-  const T* Q = static_cast<const T*>(a.Q) + token * a.qs + 8 * sub;
-  const T* K = static_cast<const T*>(a.K) + token * a.ks + 8 * sub;
-  T* Qo = static_cast<T*>(a.Qo) + token * a.qos + 8 * sub;
-  T* Ko = static_cast<T*>(a.Ko) + token * a.kos + 8 * sub;
-
-  for (int h0 = run * a.per_run * RPW; h0 < h_end; h0 += U * RPW) {
+__device__ __forceinline__ void rope_heads(const T* in, T* out, int heads, int g0, int g1, const float* weight,
+                                           const LaneDims& at, const Angles& angles, const RopeArgs& a, int hr) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int U = 4;   // head groups in flight
+  float w[8];
+  lane_weights(weight, at, w);
+  Turn turn;
+  turn.set(at, angles, w);
+  for (int g = g0; g < g1; g += U) {
     Row8<T> r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = min(h0 + u * RPW + hr, heads - 1);
-      r[u].load(h < a.h_q ? Q + static_cast<int64_t>(h) * D : K + static_cast<int64_t>(h - a.h_q) * D);
-    }
+    for (int u = 0; u < U; ++u) r[u].load(in + static_cast<int64_t>(min((g + u) * RPW + hr, heads - 1)) * D, at);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (h0 + u * RPW >= h_end) break;   // the same for the whole warp
-      const int h = h0 + u * RPW + hr;
-      float x[8];
+      if (g + u >= g1) break;   // the same for the whole warp
+      const int h = (g + u) * RPW + hr;
+      float x[8], y[8];
       r[u].get(x);
-      if (a.norm) {
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = h < a.h_q ? qw[i] : kw[i];
-        norm_row<LPR>(x, w, a.eps);
-      }
-      turn.apply(x, a.layout, lane, 8 * sub < a.rot);
-      if (h < h_end) {
-        if (h < a.h_q) Row8<T>::store(Qo + static_cast<int64_t>(h) * D, x);
-        else Row8<T>::store(Ko + static_cast<int64_t>(h - a.h_q) * D, x);
-      }
+      const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
+      turn.apply(at, x, f, y);
+      if (h < heads) Row8<T>::store(out + static_cast<int64_t>(h) * D, at, y);
     }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_kernel(const RopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes per head, heads per warp
+  const int lane = threadIdx.x & 31, sub = lane % LPR, hr = lane / LPR;
+  const int gq = (a.h_q + RPW - 1) / RPW, gk = (a.h_kv + RPW - 1) / RPW;
+  const LaneDims at(sub, a.rot, a.layout);
+  uint64_t phase[4];
+  at.phases(a.freq, sub, phase);
+  const int64_t items = static_cast<int64_t>(a.n_tokens) * a.runs;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; item < items;
+       item += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t token = item / a.runs;
+    const int g0 = static_cast<int>(item % a.runs) * a.per_run, g1 = min(g0 + a.per_run, gq + gk);
+    Angles angles;
+    angles.set<sizeof(T) == 4>(at, phase, a.rot > 0 ? __ldg(a.pos + token) : 0, a.mscale);
+    if (g0 < gq)
+      rope_heads<T, D>(static_cast<const T*>(a.Q) + token * a.qs, static_cast<T*>(a.Qo) + token * a.qos, a.h_q, g0,
+                       min(g1, gq), a.qw, at, angles, a, hr);
+    if (g1 > gq)
+      rope_heads<T, D>(static_cast<const T*>(a.K) + token * a.ks, static_cast<T*>(a.Ko) + token * a.kos, a.h_kv,
+                       max(g0 - gq, 0), g1 - gq, a.kw, at, angles, a, hr);
   }
 }
 
 template <typename T, int D>
 cudaError_t run_rope(RopeArgs a, const LaunchCtx& c) {
   constexpr int RPW = 32 / (D / 8);
-  const int groups = (a.h_q + a.h_kv + RPW - 1) / RPW;
+  const int groups = (a.h_q + RPW - 1) / RPW + (a.h_kv + RPW - 1) / RPW;
   // enough warps to fill the GPU (16 per SM) from few tokens, else all the
   // heads of a token in one run; never less than one group per run
   const int64_t want = static_cast<int64_t>(c.sm_count) * 16;
@@ -91,8 +90,8 @@ cudaError_t run_rope(RopeArgs a, const LaunchCtx& c) {
   a.per_run = static_cast<int32_t>((groups + runs - 1) / runs);
   a.runs = (groups + a.per_run - 1) / a.per_run;
   const int64_t items = static_cast<int64_t>(a.n_tokens) * a.runs;
-  const int64_t grid = (items + 7) / 8;
-  if (grid > 2147483647) return cudaErrorInvalidValue;
+  const int64_t most = static_cast<int64_t>(c.sm_count) * (sizeof(T) == 2 ? 4 : 3);   // blocks that run at a time
+  const int64_t grid = (items + 7) / 8 < most ? (items + 7) / 8 : most;
   rope_kernel<T, D><<<static_cast<unsigned>(grid), 256, 0, c.stream>>>(a);
   note_launch();
   return cudaGetLastError();

@@ -1,5 +1,5 @@
 // The norm over a head and the rotation of its first dims, for a head held by
-// d/8 neighbouring lanes of a warp, eight consecutive dims each.
+// d/8 neighbouring lanes of a warp, eight dims each.
 //
 //   y = x / sqrt(mean(x^2) + eps) * w,    (a, b) -> (a cos - b sin, b cos + a sin)
 //
@@ -8,6 +8,12 @@
 // turn), so that position * frequency wraps modulo one turn by itself and
 // the angle of position 2^31 is as exact as that of position 1 (in float32
 // the angle of position 10^6 is off by up to 0.03 rad).
+//
+// A lane's eight dims are two runs of four.  In the half layout the lanes of
+// the rotated part take dims 4 l .. and rot/2 + 4 l .., so that both dims of
+// a pair are in one lane: four angles per lane and no exchange (with eight
+// consecutive dims per lane it was eight angles and eight shuffles, and the
+// rotation of 128K tokens 745 us).  Elsewhere the two runs are neighbours.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,142 +46,153 @@ __device__ __forceinline__ void turn_of(uint64_t phase, int32_t pos, float& c, f
   }
 }
 
-// Eight consecutive elements of a row.
+// Where a lane's dims lie: runs of four at `a` and `b`.
+struct LaneDims {
+  int a, b;
+  bool rotated, half;
+  __device__ __forceinline__ LaneDims(int sub, int rot, int layout) {
+    rotated = 8 * sub < rot;
+    half = rotated && layout == SSA_ROPE_HALF;
+    a = half ? 4 * sub : 8 * sub;
+    b = half ? 4 * sub + rot / 2 : 8 * sub + 4;
+  }
+  // The lane's four phases: pairs (a + i, b + i), or (a, a + 1), (a + 2, a + 3), (b, b + 1), (b + 2, b + 3).
+  __device__ __forceinline__ void phases(const double* freq, int sub, uint64_t (&phase)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) phase[i] = rotated ? phase_of(__ldg(freq + 4 * sub + i)) : 0;
+  }
+};
+
+// Four consecutive elements.
 template <typename T>
-struct Row8;
+struct Run4;
 template <>
-struct Row8<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+struct Run4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xFFFF0000u);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* x) {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x[0], x[1]), h = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
   }
 };
 template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+struct Run4<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
+  static __device__ __forceinline__ void store(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 
-// What one lane needs of a position's rotation, for its eight dims 8*sub ..
-// 8*sub + 7 of a head (sub: the lane's place in its row).  Half layout: the
-// cos and signed sin of each dim and the lane that holds the partner dims
-// (rot is a multiple of 16, so partners lie in one lane); pairs: four cos and
-// sin.  Lanes past the rotated dims have cos 1, sin 0.
-template <bool PRECISE>
-struct Turn {
-  float c[8], s[8];
-  int partner;   // offset of the partner lane (half layout), 0 when none
+// A lane's eight dims of a head.
+template <typename T>
+struct Row8 {
+  Run4<T> a, b;
+  __device__ __forceinline__ void load(const T* row, const LaneDims& at) {
+    a.load(row + at.a);
+    b.load(row + at.b);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    a.get(x);
+    b.get(x + 4);
+  }
+  static __device__ __forceinline__ void store(T* row, const LaneDims& at, const float (&x)[8]) {
+    Run4<T>::store(row + at.a, x);
+    Run4<T>::store(row + at.b, x + 4);
+  }
+};
 
-  __device__ __forceinline__ void set(const uint64_t (&phase)[8], int sub, int rot, int layout, int32_t pos,
-                                      float mscale) {
-    partner = 0;
-    if (8 * sub >= rot) {
+__device__ __forceinline__ void lane_weights(const float* w, const LaneDims& at, float (&x)[8]) {
+  if (w) {
+    Row8<float> r;
+    r.load(w, at);
+    r.get(x);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
-      return;
-    }
-    if (layout == SSA_ROPE_HALF) {
-      const bool low = 16 * sub < rot;
-      partner = low ? rot / 16 : -(rot / 16);
+    for (int i = 0; i < 8; ++i) x[i] = 1.f;
+  }
+}
+
+// cos and sin of a lane's four pairs at a position, times mscale.
+struct Angles {
+  float c[4], s[4];
+  template <bool PRECISE>
+  __device__ __forceinline__ void set(const LaneDims& at, const uint64_t (&phase)[4], int32_t pos, float mscale) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        turn_of<PRECISE>(phase[i], pos, c[i], s[i]);
-        c[i] *= mscale;
-        s[i] *= low ? -mscale : mscale;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+      if (at.rotated) {
         turn_of<PRECISE>(phase[i], pos, c[i], s[i]);
         c[i] *= mscale;
         s[i] *= mscale;
       }
     }
   }
+};
 
-  // Rotates the row's dims in place; all lanes of the warp take part (those
-  // past the rotated dims keep theirs, infinities too).
-  __device__ __forceinline__ void apply(float (&x)[8], int layout, int lane, bool rotated) const {
-    if (layout == SSA_ROPE_HALF) {
+// A position's rotation with the weights of a head's dims folded in:
+// y[i] = x[i] * c[i] + x[partner of i] * s[i].
+struct Turn {
+  float c[8], s[8];
+
+  __device__ __forceinline__ void set(const LaneDims& at, const Angles& g, const float (&w)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xFFFFFFFFu, x[i], lane + partner);
-        if (rotated) x[i] = fmaf(y, s[i], x[i] * c[i]);
+    for (int i = 0; i < 4; ++i) {
+      // the pair's two places among the lane's eight dims
+      const int u = i, v = i + 4, p = 2 * i, q = 2 * i + 1;
+      if (at.half) {
+        c[u] = g.c[i] * w[u];
+        s[u] = -g.s[i] * w[v];
+        c[v] = g.c[i] * w[v];
+        s[v] = g.s[i] * w[u];
+      } else {
+        c[p] = g.c[i] * w[p];
+        s[p] = -g.s[i] * w[q];
+        c[q] = g.c[i] * w[q];
+        s[q] = g.s[i] * w[p];
       }
-    } else if (rotated) {
+    }
+  }
+
+  // y = r * (x turned), r the norm's factor.  A dim that does not turn takes
+  // nothing from its neighbour, infinities neither.
+  __device__ __forceinline__ void apply(const LaneDims& at, const float (&x)[8], float r, float (&y)[8]) const {
+    if (!at.rotated) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = fmaf(-b, s[i], a * c[i]);
-        x[2 * i + 1] = fmaf(a, s[i], b * c[i]);
-      }
+      for (int i = 0; i < 8; ++i) y[i] = x[i] * c[i] * r;
+    } else if (at.half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i ^ 4], s[i], x[i] * c[i]) * r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i ^ 1], s[i], x[i] * c[i]) * r;
     }
   }
 };
 
-// The phases of a lane's dims.
-__device__ __forceinline__ void lane_phases(const double* freq, int sub, int rot, int layout, uint64_t (&phase)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) phase[i] = 0;
-  if (8 * sub >= rot) return;
-  if (layout == SSA_ROPE_HALF) {
-    const int i0 = 8 * sub - (16 * sub < rot ? 0 : rot / 2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) phase[i] = phase_of(__ldg(freq + i0 + i));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) phase[i] = phase_of(__ldg(freq + 4 * sub + i));
-  }
-}
-
-// x / sqrt(mean(x^2) + eps) * w over the LPR lanes of a row.
+// 1 / sqrt(mean(x^2) + eps) over the LPR lanes of a row.
 template <int LPR>
-__device__ __forceinline__ void norm_row(float (&x)[8], const float (&w)[8], float eps) {
-  float q = 0.f;
+__device__ __forceinline__ float norm_factor(const float (&x)[8], float eps) {
+  float q = x[0] * x[0], p = x[1] * x[1];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q = fmaf(x[i], x[i], q);
+  for (int i = 2; i < 8; i += 2) {
+    q = fmaf(x[i], x[i], q);
+    p = fmaf(x[i + 1], x[i + 1], p);
+  }
+  q += p;
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
-  const float r = 1.f / sqrtf(q * (1.f / (8 * LPR)) + eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-}
-
-__device__ __forceinline__ void lane_weights(const float* w, int sub, float (&x)[8]) {
-  Row8<float> r;
-  if (w) {
-    r.load(w + 8 * sub);
-    r.get(x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 1.f;
-  }
+  return rsqrtf(fmaf(q, 1.f / (8 * LPR), eps));
 }
 
 }  // namespace ssa

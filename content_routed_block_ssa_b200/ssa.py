@@ -370,7 +370,6 @@ _ROPE_LAYOUT = {"half": SSA_ROPE_HALF, "pairs": SSA_ROPE_PAIRS}
 _ROPE_SCHEDULE = {"plain": SSA_ROPE_PLAIN, "linear": SSA_ROPE_LINEAR, "base": SSA_ROPE_BASE, "blend": SSA_ROPE_BLEND}
 _DTYPE = {"f32": SSA_F32, "bf16": SSA_BF16}
 _TORCH = {SSA_F32: torch.float32, SSA_BF16: torch.bfloat16}
-_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def rope_frequencies(rot, base=10000.0, schedule="plain", factor=1.0, trained_len=0.0, fast=32.0, slow=1.0):
@@ -413,39 +412,60 @@ def make_cache_attn_params(n_seq, n_q, max_pages, n_pages, page, h_q, h_kv, d, t
                                  scale=(1.0 / math.sqrt(d)) if scale is None else scale)
 
 
-def _arg(name, t, shape, dtype, stride=None):
-    """Address of an operand of a serving operator, after its checks: type,
-    shape, layout (dense, or with `stride` the heads dense within a token and
-    that many elements between tokens) and the current device."""
-    if t is None:
-        return None
-    if (t.dtype not in dtype) if isinstance(dtype, tuple) else (t.dtype is not dtype):
+def _refuse(name, t, dtype, shape, strides, dev):
+    """What is wrong with an operand, or its address where nothing is (an
+    empty tensor may lie anywhere, and a dimension of size 1 may have any
+    stride)."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if t.numel():
-        if stride is None:
+        if strides is None:
             if not t.is_contiguous():
                 raise ValueError(f"{name}: libssa needs a dense row-major buffer here; got strides {t.stride()}")
-        else:
-            s = t.stride()
-            if s[2] != 1 or (s[1] != shape[2] and shape[1] > 1) or (s[0] != stride and shape[0] > 1):
-                raise ValueError(f"{name}: expected strides ({stride}, {shape[2]}, 1), got {s}")
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        elif any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
+            raise ValueError(f"{name}: expected strides {strides}, got {t.stride()}")
+        if t.get_device() != dev:
             raise ValueError(f"{name}: expected a tensor on the current CUDA device, got one on {t.device}")
     return t.data_ptr()
 
 
+def _addresses(dev, specs):
+    """Addresses of a serving operator's operands, each checked: type, shape,
+    layout (dense, or the strides given) and the current device."""
+    out = []
+    for name, t, dtype, shape, strides in specs:
+        if t is None:
+            out.append(None)
+        elif t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+                (t.is_contiguous() if strides is None else t.stride() == strides):
+            out.append(t.data_ptr())
+        else:
+            out.append(_refuse(name, t, dtype, shape, strides, dev))
+    return out
+
+
+def _here(stream):
+    """(current device, stream address); without a GPU a device that no
+    tensor is on."""
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        return -2, 0
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def ssa_qk_rope(p, Q, K, q_weight, k_weight, freq, positions, Q_out, K_out, stream=None):
     """Norms of queries and keys per head and their position rotation."""
-    dt = _TORCH.get(p.dtype)
-    q, k, w = (p.n_tokens, p.h_q, p.d), (p.n_tokens, p.h_kv, p.d), (p.d,)
-    _check(lib.ssa_qk_rope(C.byref(p), _arg("Q", Q, q, dt, p.q_stride), _arg("K", K, k, dt, p.k_stride),
-                           _arg("q_weight", q_weight, w, torch.float32), _arg("k_weight", k_weight, w, torch.float32),
-                           _arg("freq", freq, (p.rot // 2,), torch.float64),
-                           _arg("positions", positions, (p.n_tokens,), torch.int32),
-                           _arg("Q_out", Q_out, q, dt, p.q_out_stride), _arg("K_out", K_out, k, dt, p.k_out_stride),
-                           _stream(stream)), "ssa_qk_rope")
+    dev, st = _here(stream)
+    dt, n, d, f32 = _TORCH.get(p.dtype), p.n_tokens, p.d, torch.float32
+    q, k, w = (n, p.h_q, d), (n, p.h_kv, d), (d,)
+    _check(lib.ssa_qk_rope(C.byref(p), *_addresses(dev, (
+        ("Q", Q, dt, q, (p.q_stride, d, 1)), ("K", K, dt, k, (p.k_stride, d, 1)),
+        ("q_weight", q_weight, f32, w, None), ("k_weight", k_weight, f32, w, None),
+        ("freq", freq, torch.float64, (p.rot // 2,), None), ("positions", positions, torch.int32, (n,), None),
+        ("Q_out", Q_out, dt, q, (p.q_out_stride, d, 1)), ("K_out", K_out, dt, k, (p.k_out_stride, d, 1)))), st),
+        "ssa_qk_rope")
 
 
 def cache_shapes(p):
@@ -453,24 +473,26 @@ def cache_shapes(p):
     return (p.n_pages, p.h_kv, p.page, p.d), (p.n_pages, p.h_kv)
 
 
-def _cache_args(p, k_cache, v_cache, k_scale, v_scale):
+def _cache_specs(p, k_cache, v_cache, k_scale, v_scale):
     codes, scales = cache_shapes(p)
-    return (_arg("k_cache", k_cache, codes, _CODES), _arg("v_cache", v_cache, codes, _CODES),
-            _arg("k_scale", k_scale, scales, torch.float32), _arg("v_scale", v_scale, scales, torch.float32))
+    # codes are bytes; a float8 tensor of them is the same memory
+    kt, vt = (torch.uint8 if t is None or t.dtype is not torch.float8_e4m3fn else t.dtype for t in (k_cache, v_cache))
+    return (("k_cache", k_cache, kt, codes, None), ("v_cache", v_cache, vt, codes, None),
+            ("k_scale", k_scale, torch.float32, scales, None), ("v_scale", v_scale, torch.float32, scales, None))
 
 
 def ssa_cache_append(p, K, V, k_weight, freq, new_start, cached, page_table, k_cache, v_cache, k_scale, v_scale,
                      bad_count=None, stream=None):
     """Appends keys (normed, rotated) and values to the paged 8-bit cache."""
-    dt, kv = _TORCH.get(p.dtype), (p.n_tokens, p.h_kv, p.d)
-    _check(lib.ssa_cache_append(C.byref(p), _arg("K", K, kv, dt, p.k_stride), _arg("V", V, kv, dt, p.v_stride),
-                                _arg("k_weight", k_weight, (p.d,), torch.float32),
-                                _arg("freq", freq, (p.rot // 2,), torch.float64),
-                                _arg("new_start", new_start, (p.n_seq + 1,), torch.int32),
-                                _arg("cached", cached, (p.n_seq,), torch.int32),
-                                _arg("page_table", page_table, (p.n_seq, p.max_pages), torch.int32),
-                                *_cache_args(p, k_cache, v_cache, k_scale, v_scale),
-                                _arg("bad_count", bad_count, (1,), torch.int32), _stream(stream)), "ssa_cache_append")
+    dev, st = _here(stream)
+    dt, n, d, i32 = _TORCH.get(p.dtype), p.n_seq, p.d, torch.int32
+    kv = (p.n_tokens, p.h_kv, d)
+    _check(lib.ssa_cache_append(C.byref(p), *_addresses(dev, (
+        ("K", K, dt, kv, (p.k_stride, d, 1)), ("V", V, dt, kv, (p.v_stride, d, 1)),
+        ("k_weight", k_weight, torch.float32, (d,), None), ("freq", freq, torch.float64, (p.rot // 2,), None),
+        ("new_start", new_start, i32, (n + 1,), None), ("cached", cached, i32, (n,), None),
+        ("page_table", page_table, i32, (n, p.max_pages), None), *_cache_specs(p, k_cache, v_cache, k_scale, v_scale),
+        ("bad_count", bad_count, i32, (1,), None))), st), "ssa_cache_append")
 
 
 def ssa_cache_attn_workspace_size(p) -> int:
@@ -480,15 +502,15 @@ def ssa_cache_attn_workspace_size(p) -> int:
 def ssa_cache_attn(p, Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale, block_idx, O, lse=None,
                    bad_count=None, ws=None, stream=None):
     """Attention of new tokens over the paged 8-bit cache."""
-    q = (p.n_seq, p.n_q, p.h_q, p.d)
-    _check(lib.ssa_cache_attn(C.byref(p), _arg("Q", Q, q, torch.bfloat16),
-                              _arg("page_table", page_table, (p.n_seq, p.max_pages), torch.int32),
-                              _arg("kv_len", kv_len, (p.n_seq,), torch.int32),
-                              *_cache_args(p, k_cache, v_cache, k_scale, v_scale),
-                              _arg("block_idx", block_idx, (p.n_seq, p.n_q, p.h_kv, p.topk), torch.int32),
-                              _arg("O", O, q, torch.bfloat16), _arg("lse", lse, q[:3], torch.float32),
-                              _arg("bad_count", bad_count, (1,), torch.int32), _ptr(ws), _nbytes(ws),
-                              _stream(stream)), "ssa_cache_attn")
+    dev, st = _here(stream)
+    n, i32 = p.n_seq, torch.int32
+    q = (n, p.n_q, p.h_q, p.d)
+    _check(lib.ssa_cache_attn(C.byref(p), *_addresses(dev, (
+        ("Q", Q, torch.bfloat16, q, None), ("page_table", page_table, i32, (n, p.max_pages), None),
+        ("kv_len", kv_len, i32, (n,), None), *_cache_specs(p, k_cache, v_cache, k_scale, v_scale),
+        ("block_idx", block_idx, i32, (n, p.n_q, p.h_kv, p.topk), None), ("O", O, torch.bfloat16, q, None),
+        ("lse", lse, torch.float32, q[:3], None), ("bad_count", bad_count, i32, (1,), None),
+        ("ws", ws, torch.uint8, ws.shape if ws is not None else None, None))), _nbytes(ws), st), "ssa_cache_attn")
 
 
 def make_prompt_params(n_seq, n_q, n_kv, h_q, h_kv, d, q_stride=None, k_stride=None, v_stride=None, o_stride=None,
@@ -504,14 +526,14 @@ def make_prompt_params(n_seq, n_q, n_kv, h_q, h_kv, d, q_stride=None, k_stride=N
 
 def ssa_prompt_attn(p, Q, K, V, q_start, kv_start, O, lse=None, stream=None):
     """Causal attention over packed prompts of different lengths."""
-    q, kv = (p.n_q, p.h_q, p.d), (p.n_kv, p.h_kv, p.d)
-    _check(lib.ssa_prompt_attn(C.byref(p), _arg("Q", Q, q, torch.bfloat16, p.q_stride),
-                               _arg("K", K, kv, torch.bfloat16, p.k_stride),
-                               _arg("V", V, kv, torch.bfloat16, p.v_stride),
-                               _arg("q_start", q_start, (p.n_seq + 1,), torch.int32),
-                               _arg("kv_start", kv_start, (p.n_seq + 1,), torch.int32),
-                               _arg("O", O, q, torch.bfloat16, p.o_stride),
-                               _arg("lse", lse, q[:2], torch.float32), _stream(stream)), "ssa_prompt_attn")
+    dev, st = _here(stream)
+    bf16, d, starts = torch.bfloat16, p.d, (p.n_seq + 1,)
+    q, kv = (p.n_q, p.h_q, d), (p.n_kv, p.h_kv, d)
+    _check(lib.ssa_prompt_attn(C.byref(p), *_addresses(dev, (
+        ("Q", Q, bf16, q, (p.q_stride, d, 1)), ("K", K, bf16, kv, (p.k_stride, d, 1)),
+        ("V", V, bf16, kv, (p.v_stride, d, 1)), ("q_start", q_start, torch.int32, starts, None),
+        ("kv_start", kv_start, torch.int32, starts, None), ("O", O, bf16, q, (p.o_stride, d, 1)),
+        ("lse", lse, torch.float32, q[:2], None))), st), "ssa_prompt_attn")
 
 
 SITE_SELFTEST = 0x7F1

@@ -8,8 +8,8 @@
 // floor(tokens / page) + 2 pages, so the ranges never meet, and a warp finds
 // its sequence by a 32-way search without a pass over the lengths.
 //
-// Two kernels, by the tokens per sequence (see launch_cache_append): a block
-// per (unit, kv-head, K or V) that keeps the page's tokens in registers
+// Two kernels, by the tokens per sequence (see run_append): a block per
+// (unit, K or V, run of kv-heads) that keeps the page's tokens in registers
 // between the maximum and the rounding (each element is read once), and, for
 // decode steps, a warp per (unit, kv-head, K or V).  Bytes bound the first,
 // launch and the chain of dependent index loads the second.
@@ -22,11 +22,14 @@
 namespace ssa {
 namespace {
 
+constexpr int kKeep = 4;   // rows of a page per thread
+
 struct AppendCfg {
   AppendArgs g;
   int64_t k_stride, v_stride;
   int32_t n_tokens, n_seq, max_pages, n_pages, h_kv, rot, layout, norm;
   int32_t n_units;
+  int32_t runs, per_run;   // runs of kv-heads per unit, kv-heads per run
   float eps, mscale;
 };
 
@@ -82,18 +85,19 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t un
   return u;
 }
 
-// The largest |x| of finite elements so far (fmaxf leaves NaN out).
-__device__ __forceinline__ float finite_amax(const float (&x)[8], float m) {
-  float r = m;
+// The largest finite |x| * f of a row's elements and m (fmaxf leaves NaN out).
+__device__ __forceinline__ float finite_amax(const float (&x)[8], float f, float m) {
+  float r = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r = fmaxf(r, fabsf(x[i]));
-  if (r == INFINITY) {
-    r = m;
+  for (int i = 1; i < 8; ++i) r = fmaxf(r, fabsf(x[i]));
+  r *= f;
+  if (!(r < INFINITY)) {   // among them an infinity (or all NaN): one by one
+    r = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (fabsf(x[i]) != INFINITY) r = fmaxf(r, fabsf(x[i]));
+      if (fabsf(x[i]) * f < INFINITY) r = fmaxf(r, fabsf(x[i]) * f);
   }
-  return r;
+  return fmaxf(m, r);
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* row, const LaneDims& at, const float (&x)[8], float inv) {
@@ -121,85 +125,102 @@ __device__ __forceinline__ void round_again(uint8_t* p, float down) {
   *reinterpret_cast<uint4*>(p) = v;
 }
 
-// One row's eight dims of this lane in float32: the key normed and rotated,
-// the value as it is.
+// One row's eight dims of this lane in float32: the key weighted and rotated,
+// the value as it is.  Returns the norm's factor, which the caller applies
+// to the row's maximum and, with the page's scale, to its codes: one product
+// per element for both.
 template <typename T, int LPR>
-__device__ __forceinline__ void append_row(const AppendCfg& a, bool is_k, const Row8<T>& r, const LaneDims& at,
-                                           const float (&w)[8], const uint64_t (&phase)[4], int pos, float (&y)[8]) {
-  if (!is_k) {
-    r.get(y);
-    return;
-  }
-  float x[8];
+__device__ __forceinline__ float append_row(const AppendCfg& a, bool is_k, const Row8<T>& r, const LaneDims& at,
+                                            const float (&w)[8], const Angles& g, float (&x)[8]) {
   r.get(x);
+  if (!is_k) return 1.f;
   const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
-  Angles g;
-  g.set<sizeof(T) == 4>(at, phase, pos, a.mscale);
-  Turn t;
-  t.set(at, g, w);
-  t.apply(at, x, f, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= w[i];
+  g.turn(at, x);
+  return f;
 }
 
 // The page's exponent, and the rounding of what it held when that grows.
 template <int D>
-__device__ __forceinline__ int page_exponent(const AppendUnit& u, float amax, float* scale, uint8_t* codes, int thread,
+__device__ __forceinline__ int page_exponent(const AppendUnit& u, float amax, float old, uint8_t* codes, int thread,
                                              int threads) {
   const int e_new = scale_exponent(amax);
   if (u.slot0 == 0) return e_new;
-  const int e_old = exponent_of(*scale);
+  const int e_old = exponent_of(old);
   if (e_new <= e_old) return e_old;
   const float down = pow2(e_old - e_new);
   for (int i = thread; i < u.slot0 * (D / 16); i += threads) round_again(codes + i * 16, down);
   return e_new;
 }
 
-// Prompts: a block per (unit, kv-head, K or V), the page's rows in registers.
+// Prompts: a block per (unit, K or V, run of kv-heads), the page's rows of a
+// head in registers, the next head's on their way.  The unit is looked up and
+// the angles are computed once for all the heads of the run.  (A block per
+// kv-head spent most of its life in the chain of index loads: 205 us for 64K
+// tokens of eight heads.)
 template <typename T, int D, int P>
-__global__ void __launch_bounds__(256) append_page_kernel(const AppendCfg a) {
-  constexpr int LPR = D / 8, ROWS = 256 / LPR, KEEP = P / ROWS;
-  __shared__ float red[8];
+__global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1 : 2) append_page_kernel(const AppendCfg a) {
+  constexpr int LPR = D / 8, KEEP = kKeep, THREADS = P * LPR / KEEP, ROWS = THREADS / LPR;
+  __shared__ float red[2][THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, sub = lane % LPR;
   const int row = threadIdx.x / LPR;
-  const int head = blockIdx.x % a.h_kv;
-  const int64_t unit = blockIdx.x / a.h_kv;
-  const bool is_k = blockIdx.y == 0;
-  const AppendUnit u = append_unit<P>(a, unit, head == 0 && is_k && warp == 0);
+  const bool is_k = (blockIdx.x & 1) == 0;   // keys take longer: the two kinds take turns
+  const int item = static_cast<int>(blockIdx.x >> 1);
+  const int h0 = item % a.runs * a.per_run, h1 = min(h0 + a.per_run, a.h_kv);
+  const AppendUnit u = append_unit<P>(a, item / a.runs, h0 == 0 && is_k && warp == 0);
   if (u.page < 0) return;
-  const T* src = is_k ? static_cast<const T*>(a.g.K) + static_cast<int64_t>(u.t0) * a.k_stride
-                      : static_cast<const T*>(a.g.V) + static_cast<int64_t>(u.t0) * a.v_stride;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
-  src += static_cast<int64_t>(head) * D;
   const LaneDims at(sub, is_k ? a.rot : 0, a.layout);
+  const T* src[KEEP];
   Row8<T> r[KEEP];
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) r[k].load(src + static_cast<int64_t>(min(row + k * ROWS, u.n - 1)) * stride, at);
-  float w[8];
-  uint64_t phase[4];
-  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
-  at.phases(a.g.freq, sub, phase);
-  float x[KEEP][8];
-  float amax = 0.f;
-#pragma unroll
   for (int k = 0; k < KEEP; ++k) {   // rows past the last repeat it: the same maximum
-    append_row<T, LPR>(a, is_k, r[k], at, w, phase, u.pos0 + min(row + k * ROWS, u.n - 1), x[k]);
-    amax = finite_amax(x[k], amax);
+    src[k] = static_cast<const T*>(is_k ? a.g.K : a.g.V) + (u.t0 + min(row + k * ROWS, u.n - 1)) * stride +
+             static_cast<int64_t>(h0) * D;
+    r[k].load(src[k], at);
   }
+  float w[8];
+  lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
+  Angles angles[KEEP];
+  if (is_k) {
+    uint64_t phase[4];
+    at.phases(a.g.freq, sub, phase);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-  if (lane == 0) red[warp] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, red[i]);
-  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + head;
+    for (int k = 0; k < KEEP; ++k)
+      angles[k].set<sizeof(T) == 4>(at, phase, u.pos0 + min(row + k * ROWS, u.n - 1), a.mscale);
+  }
+  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + h0;
   uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
   float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
-  const int e = page_exponent<D>(u, amax, scale, codes, threadIdx.x, 256);
-  const float inv = pow2(-e);
+  for (int h = h0; h < h1; ++h, codes += P * D, ++scale) {
+    const float old = u.slot0 > 0 ? *scale : 0.f;
+    float x[KEEP][8], f[KEEP];
+    float amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k)
-    if (row + k * ROWS < u.n) store_codes(codes + (u.slot0 + row + k * ROWS) * D, at, x[k], inv);
-  __syncthreads();   // every thread has read the old scale
-  if (threadIdx.x == 0) *scale = pow2(e);
+    for (int k = 0; k < KEEP; ++k) {
+      f[k] = append_row<T, LPR>(a, is_k, r[k], at, w, angles[k], x[k]);
+      amax = finite_amax(x[k], f[k], amax);
+    }
+    if (h + 1 < h1)
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k) {
+        src[k] += D;
+        r[k].load(src[k], at);
+      }
+    amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
+    if (lane == 0) red[h & 1][warp] = amax;
+    __syncthreads();   // the maxima are there, and every thread has the old scale
+    amax = __uint_as_float(
+        __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(red[h & 1][lane % (THREADS / 32)])));
+    const int e = page_exponent<D>(u, amax, old, codes, threadIdx.x, THREADS);
+    const float inv = pow2(-e);
+    uint8_t* to = codes + (u.slot0 + row) * D;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (row + k * ROWS < u.n) store_codes(to + k * ROWS * D, at, x[k], f[k] * inv);
+    if (threadIdx.x == 0) *scale = pow2(e);
+  }
 }
 
 // Decode steps: a warp per (unit, kv-head, K or V).  More rows than one pass
@@ -224,28 +245,29 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   uint64_t phase[4];
   lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
   at.phases(a.g.freq, sub, phase);
-  float x[8];
+  float x[8], f = 1.f;
   const auto value = [&](int i0) {
     const int i = min(i0 + row, u.n - 1);
     Row8<T> r;
     r.load(src + static_cast<int64_t>(i) * stride, at);
-    append_row<T, LPR>(a, is_k, r, at, w, phase, u.pos0 + i, x);
+    Angles g;
+    if (is_k) g.set<sizeof(T) == 4>(at, phase, u.pos0 + i, a.mscale);
+    f = append_row<T, LPR>(a, is_k, r, at, w, g, x);
   };
   float amax = 0.f;
   for (int i0 = 0; i0 < u.n; i0 += RPW) {
     value(i0);
-    amax = finite_amax(x, amax);
+    amax = finite_amax(x, f, amax);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
   const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + head;
   uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
   float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
-  const int e = page_exponent<D>(u, amax, scale, codes, lane, 32);
+  const int e = page_exponent<D>(u, amax, u.slot0 > 0 ? *scale : 0.f, codes, lane, 32);
   const float inv = pow2(-e);
   for (int i0 = 0; i0 < u.n; i0 += RPW) {
     if (u.n > RPW) value(i0);
-    if (i0 + row < u.n) store_codes(codes + (u.slot0 + i0 + row) * D, at, x, inv);
+    if (i0 + row < u.n) store_codes(codes + (u.slot0 + i0 + row) * D, at, x, f * inv);
   }
   __syncwarp();
   if (lane == 0) *scale = pow2(e);
@@ -260,8 +282,15 @@ cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
     const int64_t grid = (units * 2 * a.h_kv + 7) / 8;
     append_few_kernel<T, D, P><<<static_cast<unsigned>(grid), 256, 0, c.stream>>>(a);
   } else {
-    const dim3 grid(static_cast<unsigned>(units * a.h_kv), 2);
-    append_page_kernel<T, D, P><<<grid, 256, 0, c.stream>>>(a);
+    // all kv-heads in one run where the units alone give every SM work for
+    // four rounds of two blocks, else as many runs as that takes
+    int64_t runs = (8 * static_cast<int64_t>(c.sm_count) + 2 * units - 1) / (2 * units);
+    if (runs > a.h_kv) runs = a.h_kv;
+    a.per_run = static_cast<int32_t>((a.h_kv + runs - 1) / runs);
+    a.runs = (a.h_kv + a.per_run - 1) / a.per_run;
+    const int64_t grid = units * a.runs * 2;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    append_page_kernel<T, D, P><<<static_cast<unsigned>(grid), P * D / 8 / kKeep, 0, c.stream>>>(a);
   }
   note_launch();
   return cudaGetLastError();

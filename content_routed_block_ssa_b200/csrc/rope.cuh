@@ -49,12 +49,13 @@ __device__ __forceinline__ void turn_of(uint64_t phase, int32_t pos, float& c, f
 // Where a lane's dims lie: runs of four at `a` and `b`.
 struct LaneDims {
   int a, b;
-  bool rotated, half;
+  bool rotated;   // this lane's dims turn
+  bool half;      // the layout, the same for all lanes
   __device__ __forceinline__ LaneDims(int sub, int rot, int layout) {
     rotated = 8 * sub < rot;
-    half = rotated && layout == SSA_ROPE_HALF;
-    a = half ? 4 * sub : 8 * sub;
-    b = half ? 4 * sub + rot / 2 : 8 * sub + 4;
+    half = layout == SSA_ROPE_HALF;
+    a = rotated && half ? 4 * sub : 8 * sub;
+    b = rotated && half ? 4 * sub + rot / 2 : 8 * sub + 4;
   }
   // The lane's four phases: pairs (a + i, b + i), or (a, a + 1), (a + 2, a + 3), (b, b + 1), (b + 2, b + 3).
   __device__ __forceinline__ void phases(const double* freq, int sub, uint64_t (&phase)[4]) const {
@@ -135,6 +136,26 @@ struct Angles {
         turn_of<PRECISE>(phase[i], pos, c[i], s[i]);
         c[i] *= mscale;
         s[i] *= mscale;
+      }
+    }
+  }
+  // Turns a row's dims in place; a dim that does not turn takes nothing from
+  // its neighbour, infinities neither.
+  __device__ __forceinline__ void turn(const LaneDims& at, float (&x)[8]) const {
+    if (at.half) {
+      if (at.rotated)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = x[i], b = x[i + 4];
+          x[i] = fmaf(-b, s[i], a * c[i]);
+          x[i + 4] = fmaf(a, s[i], b * c[i]);
+        }
+    } else if (at.rotated) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = fmaf(-b, s[i], a * c[i]);
+        x[2 * i + 1] = fmaf(a, s[i], b * c[i]);
       }
     }
   }

@@ -9,6 +9,7 @@ to, and importing this module fails if ``libssa.so`` has not been built.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 
@@ -412,11 +413,12 @@ def make_cache_attn_params(n_seq, n_q, max_pages, n_pages, page, h_q, h_kv, d, t
                                  scale=(1.0 / math.sqrt(d)) if scale is None else scale)
 
 
-def _refuse(name, t, dtype, shape, strides, dev):
+def _refuse(spec, t, dev):
     """What is wrong with an operand, or its address where nothing is (an
-    empty tensor may lie anywhere, and a dimension of size 1 may have any
-    stride)."""
-    if t.dtype is not dtype:
+    empty tensor may lie anywhere, a dimension of size 1 may have any stride,
+    and e4m3 codes may come as bytes or as float8)."""
+    name, dtype, shape, strides = spec
+    if t.dtype is not dtype and not (dtype is torch.uint8 and t.dtype is torch.float8_e4m3fn):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
@@ -431,18 +433,18 @@ def _refuse(name, t, dtype, shape, strides, dev):
     return t.data_ptr()
 
 
-def _addresses(dev, specs):
-    """Addresses of a serving operator's operands, each checked: type, shape,
-    layout (dense, or the strides given) and the current device."""
+def _addresses(dev, specs, tensors):
+    """Addresses of a serving operator's operands, each checked against its
+    (name, type, shape, strides or None for dense) and the current device."""
     out = []
-    for name, t, dtype, shape, strides in specs:
+    for spec, t in zip(specs, tensors):
         if t is None:
             out.append(None)
-        elif t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
-                (t.is_contiguous() if strides is None else t.stride() == strides):
+        elif t.dtype is spec[1] and t.shape == spec[2] and t.get_device() == dev and \
+                (t.is_contiguous() if spec[3] is None else t.stride() == spec[3]):
             out.append(t.data_ptr())
         else:
-            out.append(_refuse(name, t, dtype, shape, strides, dev))
+            out.append(_refuse(spec, t, dev))
     return out
 
 
@@ -455,17 +457,25 @@ def _here(stream):
     return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+# The operands' types and shapes follow from the parameters alone; they are
+# worked out once per set of parameters (the struct's bytes).
+
+@functools.lru_cache(maxsize=256)
+def _rope_specs(raw):
+    p = ssa_rope_params.from_buffer_copy(raw)
+    dt, n, d = _TORCH.get(p.dtype), p.n_tokens, p.d
+    q, k = (n, p.h_q, d), (n, p.h_kv, d)
+    return (("Q", dt, q, (p.q_stride, d, 1)), ("K", dt, k, (p.k_stride, d, 1)),
+            ("q_weight", torch.float32, (d,), None), ("k_weight", torch.float32, (d,), None),
+            ("freq", torch.float64, (p.rot // 2,), None), ("positions", torch.int32, (n,), None),
+            ("Q_out", dt, q, (p.q_out_stride, d, 1)), ("K_out", dt, k, (p.k_out_stride, d, 1)))
+
+
 def ssa_qk_rope(p, Q, K, q_weight, k_weight, freq, positions, Q_out, K_out, stream=None):
     """Norms of queries and keys per head and their position rotation."""
     dev, st = _here(stream)
-    dt, n, d, f32 = _TORCH.get(p.dtype), p.n_tokens, p.d, torch.float32
-    q, k, w = (n, p.h_q, d), (n, p.h_kv, d), (d,)
-    _check(lib.ssa_qk_rope(C.byref(p), *_addresses(dev, (
-        ("Q", Q, dt, q, (p.q_stride, d, 1)), ("K", K, dt, k, (p.k_stride, d, 1)),
-        ("q_weight", q_weight, f32, w, None), ("k_weight", k_weight, f32, w, None),
-        ("freq", freq, torch.float64, (p.rot // 2,), None), ("positions", positions, torch.int32, (n,), None),
-        ("Q_out", Q_out, dt, q, (p.q_out_stride, d, 1)), ("K_out", K_out, dt, k, (p.k_out_stride, d, 1)))), st),
-        "ssa_qk_rope")
+    at = _addresses(dev, _rope_specs(bytes(p)), (Q, K, q_weight, k_weight, freq, positions, Q_out, K_out))
+    _check(lib.ssa_qk_rope(C.byref(p), *at, st), "ssa_qk_rope")
 
 
 def cache_shapes(p):
@@ -473,44 +483,56 @@ def cache_shapes(p):
     return (p.n_pages, p.h_kv, p.page, p.d), (p.n_pages, p.h_kv)
 
 
-def _cache_specs(p, k_cache, v_cache, k_scale, v_scale):
+def _cache_specs(p):
     codes, scales = cache_shapes(p)
-    # codes are bytes; a float8 tensor of them is the same memory
-    kt, vt = (torch.uint8 if t is None or t.dtype is not torch.float8_e4m3fn else t.dtype for t in (k_cache, v_cache))
-    return (("k_cache", k_cache, kt, codes, None), ("v_cache", v_cache, vt, codes, None),
-            ("k_scale", k_scale, torch.float32, scales, None), ("v_scale", v_scale, torch.float32, scales, None))
+    return (("page_table", torch.int32, (p.n_seq, p.max_pages), None), ("k_cache", torch.uint8, codes, None),
+            ("v_cache", torch.uint8, codes, None), ("k_scale", torch.float32, scales, None),
+            ("v_scale", torch.float32, scales, None), ("bad_count", torch.int32, (1,), None))
+
+
+@functools.lru_cache(maxsize=256)
+def _append_specs(raw):
+    p = ssa_append_params.from_buffer_copy(raw)
+    dt, d, kv = _TORCH.get(p.dtype), p.d, (p.n_tokens, p.h_kv, p.d)
+    return (("K", dt, kv, (p.k_stride, d, 1)), ("V", dt, kv, (p.v_stride, d, 1)),
+            ("k_weight", torch.float32, (d,), None), ("freq", torch.float64, (p.rot // 2,), None),
+            ("new_start", torch.int32, (p.n_seq + 1,), None), ("cached", torch.int32, (p.n_seq,), None),
+            *_cache_specs(p))
 
 
 def ssa_cache_append(p, K, V, k_weight, freq, new_start, cached, page_table, k_cache, v_cache, k_scale, v_scale,
                      bad_count=None, stream=None):
     """Appends keys (normed, rotated) and values to the paged 8-bit cache."""
     dev, st = _here(stream)
-    dt, n, d, i32 = _TORCH.get(p.dtype), p.n_seq, p.d, torch.int32
-    kv = (p.n_tokens, p.h_kv, d)
-    _check(lib.ssa_cache_append(C.byref(p), *_addresses(dev, (
-        ("K", K, dt, kv, (p.k_stride, d, 1)), ("V", V, dt, kv, (p.v_stride, d, 1)),
-        ("k_weight", k_weight, torch.float32, (d,), None), ("freq", freq, torch.float64, (p.rot // 2,), None),
-        ("new_start", new_start, i32, (n + 1,), None), ("cached", cached, i32, (n,), None),
-        ("page_table", page_table, i32, (n, p.max_pages), None), *_cache_specs(p, k_cache, v_cache, k_scale, v_scale),
-        ("bad_count", bad_count, i32, (1,), None))), st), "ssa_cache_append")
+    at = _addresses(dev, _append_specs(bytes(p)), (K, V, k_weight, freq, new_start, cached, page_table, k_cache,
+                                                   v_cache, k_scale, v_scale, bad_count))
+    _check(lib.ssa_cache_append(C.byref(p), *at, st), "ssa_cache_append")
 
 
 def ssa_cache_attn_workspace_size(p) -> int:
     return int(lib.ssa_cache_attn_workspace_size(C.byref(p)))
 
 
+@functools.lru_cache(maxsize=256)
+def _cache_attn_specs(raw):
+    p = ssa_cache_attn_params.from_buffer_copy(raw)
+    q = (p.n_seq, p.n_q, p.h_q, p.d)
+    table, kc, vc, ks, vs, bad = _cache_specs(p)
+    return (("Q", torch.bfloat16, q, None), table, ("kv_len", torch.int32, (p.n_seq,), None), kc, vc, ks, vs,
+            ("block_idx", torch.int32, (p.n_seq, p.n_q, p.h_kv, p.topk), None), ("O", torch.bfloat16, q, None),
+            ("lse", torch.float32, q[:3], None), bad)
+
+
 def ssa_cache_attn(p, Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale, block_idx, O, lse=None,
                    bad_count=None, ws=None, stream=None):
     """Attention of new tokens over the paged 8-bit cache."""
     dev, st = _here(stream)
-    n, i32 = p.n_seq, torch.int32
-    q = (n, p.n_q, p.h_q, p.d)
-    _check(lib.ssa_cache_attn(C.byref(p), *_addresses(dev, (
-        ("Q", Q, torch.bfloat16, q, None), ("page_table", page_table, i32, (n, p.max_pages), None),
-        ("kv_len", kv_len, i32, (n,), None), *_cache_specs(p, k_cache, v_cache, k_scale, v_scale),
-        ("block_idx", block_idx, i32, (n, p.n_q, p.h_kv, p.topk), None), ("O", O, torch.bfloat16, q, None),
-        ("lse", lse, torch.float32, q[:3], None), ("bad_count", bad_count, i32, (1,), None),
-        ("ws", ws, torch.uint8, ws.shape if ws is not None else None, None))), _nbytes(ws), st), "ssa_cache_attn")
+    at = _addresses(dev, _cache_attn_specs(bytes(p)), (Q, page_table, kv_len, k_cache, v_cache, k_scale, v_scale,
+                                                       block_idx, O, lse, bad_count))
+    if ws is not None and ws.numel() and (ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws: expected a dense buffer on the current CUDA device")
+    _check(lib.ssa_cache_attn(C.byref(p), *at, None if ws is None else ws.data_ptr(), _nbytes(ws), st),
+           "ssa_cache_attn")
 
 
 def make_prompt_params(n_seq, n_q, n_kv, h_q, h_kv, d, q_stride=None, k_stride=None, v_stride=None, o_stride=None,
@@ -524,16 +546,22 @@ def make_prompt_params(n_seq, n_q, n_kv, h_q, h_kv, d, q_stride=None, k_stride=N
                              scale=(1.0 / math.sqrt(d)) if scale is None else scale)
 
 
+@functools.lru_cache(maxsize=256)
+def _prompt_specs(raw):
+    p = ssa_prompt_params.from_buffer_copy(raw)
+    bf16, d, starts = torch.bfloat16, p.d, (p.n_seq + 1,)
+    q, kv = (p.n_q, p.h_q, d), (p.n_kv, p.h_kv, d)
+    return (("Q", bf16, q, (p.q_stride, d, 1)), ("K", bf16, kv, (p.k_stride, d, 1)),
+            ("V", bf16, kv, (p.v_stride, d, 1)), ("q_start", torch.int32, starts, None),
+            ("kv_start", torch.int32, starts, None), ("O", bf16, q, (p.o_stride, d, 1)),
+            ("lse", torch.float32, q[:2], None))
+
+
 def ssa_prompt_attn(p, Q, K, V, q_start, kv_start, O, lse=None, stream=None):
     """Causal attention over packed prompts of different lengths."""
     dev, st = _here(stream)
-    bf16, d, starts = torch.bfloat16, p.d, (p.n_seq + 1,)
-    q, kv = (p.n_q, p.h_q, d), (p.n_kv, p.h_kv, d)
-    _check(lib.ssa_prompt_attn(C.byref(p), *_addresses(dev, (
-        ("Q", Q, bf16, q, (p.q_stride, d, 1)), ("K", K, bf16, kv, (p.k_stride, d, 1)),
-        ("V", V, bf16, kv, (p.v_stride, d, 1)), ("q_start", q_start, torch.int32, starts, None),
-        ("kv_start", kv_start, torch.int32, starts, None), ("O", O, bf16, q, (p.o_stride, d, 1)),
-        ("lse", lse, torch.float32, q[:2], None))), st), "ssa_prompt_attn")
+    at = _addresses(dev, _prompt_specs(bytes(p)), (Q, K, V, q_start, kv_start, O, lse))
+    _check(lib.ssa_prompt_attn(C.byref(p), *at, st), "ssa_prompt_attn")
 
 
 SITE_SELFTEST = 0x7F1

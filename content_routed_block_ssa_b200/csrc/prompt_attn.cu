@@ -28,6 +28,13 @@
 namespace ssa {
 namespace {
 
+// Of eight pairs of exponentials, how many go to the FMA pipe.
+constexpr int kPolyOf8 = 2;
+constexpr float kExp1 = 0.69312418f, kExp2 = 0.24024099f, kExp3 = 0.055906426f, kExp4 = 0.0095828529f;
+// Registers per thread of the softmax warps and of the others, traded at the
+// start: 2 * 208 + 88 = 3 * 168, what a block of 384 threads starts with.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+
 template <int D>
 struct PromptShape {
   static constexpr int ROW = 128;                     // bytes of a 64-dim swizzled row
@@ -35,10 +42,10 @@ struct PromptShape {
   static constexpr int TILE = 128 * ROW * HALVES;     // 128 rows (queries x heads, or keys)
   static constexpr int SLOTS = D == 128 ? 5 : 8;      // ring of K and V tiles
   static constexpr int BARS = 2 * TILE + SLOTS * TILE;
-  static constexpr int NBAR = 1 + 2 * SLOTS + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 1 + 2 * SLOTS + 2 + 4 + 2 + 1;
   static constexpr int USED = BARS + NBAR * 8 + 16;
   static constexpr int SMEM = USED + 1024 < 232448 ? USED + 1024 : 232448;
-  static constexpr int THREADS = 320;                 // 2 x 4 softmax warps, loads, products
+  static constexpr int THREADS = 384;                 // 2 x 4 softmax warps; loads, products and two idle
   static_assert(USED <= 232448, "shared memory");
 };
 
@@ -140,6 +147,41 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// max of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^x of a pair on the FMA pipe, x <= 2^7: x = n + f with |f| <= 1/2, 2^f by a
+// polynomial (least largest relative error on [-1/2, 1/2] with 2^0 = 1, fitted
+// for this kernel: 2^-18.4), n added to the exponent.  x below -127 (-inf of
+// masked keys) gives 0 exactly: n = -127 and f = 0 leave no bits.
+__device__ __forceinline__ void poly_exp2(uint64_t x2, float& x, float& y) {
+  unpair(x2, x, y);
+  x2 = pair(fmaxf(x, -127.f), fmaxf(y, -127.f));
+  const uint64_t t2 = add2(x2, pair(12582912.f, 12582912.f));   // 1.5 * 2^23: rounds to an integer
+  const uint64_t f2 = fma2(add2(t2, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x2);
+  uint64_t p2 = fma2(pair(kExp4, kExp4), f2, pair(kExp3, kExp3));
+  p2 = fma2(p2, f2, pair(kExp2, kExp2));
+  p2 = fma2(p2, f2, pair(kExp1, kExp1));
+  p2 = fma2(p2, f2, pair(1.f, 1.f));
+  float p, q, s, t;
+  unpair(p2, p, q);
+  unpair(t2, s, t);
+  x = __uint_as_float(__float_as_uint(p) + (__float_as_uint(s) << 23));
+  y = __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));
+}
+
 __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
@@ -179,7 +221,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptArgs a) {
   using C = PromptShape<D>;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0);   // known to be uniform
+  const int lane = threadIdx.x & 31;
   const int kvh = blockIdx.x % a.h_kv;
   const PromptUnit u = prompt_unit(a, a.n_units - 1 - static_cast<int>(blockIdx.x / a.h_kv));
   if (!u.any) return;   // the same for every warp
@@ -197,8 +240,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   uint64_t* full = bars + 1;
   uint64_t* empty = full + C::SLOTS;
   uint64_t* s_full = empty + C::SLOTS;   // [2 tiles]
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;         // the tile's last product is done
+  uint64_t* p_full = s_full + 2;         // [2 tiles][2 halves of the step's keys]
+  uint64_t* o_full = p_full + 4;         // the tile's last product is done
   uint64_t* mma_done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
 
@@ -215,7 +258,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[t], 4); mbar_init(&o_full[t], 1); }
+    for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[2 * t], 4); mbar_init(&p_full[2 * t + 1], 4); mbar_init(&o_full[t], 1); }
     mbar_init(mma_done, 1);
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
@@ -231,6 +274,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;   // S of tile t at 128 t, O at 256 + 128 t
 
+  if (warp >= 8) {
+    // this warpgroup hands registers to the two softmax warpgroups
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 8) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && n > 0) {
@@ -261,58 +307,81 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 128);
-      constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);   // V is MN-major
-      const uint32_t sQ_u = smem_u32(sQ), ring_u = smem_u32(ring);
-      const auto wait_load = [&](int i) {
-        return mbar_wait(&full[i % C::SLOTS], (i / C::SLOTS) & 1, a.err, SITE_PROMPT_MMA);
-      };
-      const auto scores = [&](int t, int j) {   // S of tile t, step j (K is load 2 j)
-        const uint32_t k_u = ring_u + ((2 * j) % C::SLOTS) * C::TILE;
+    // The whole warp runs the loop, so that descriptors and counters stay in
+    // uniform registers, and one lane issues: with one lane running all of it
+    // the issue, not the tensor core, set the pace (about 95 clocks per
+    // product of 64).
+    const bool leader = elect_one();
+    constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 128);
+    constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);   // V is MN-major
+    const uint64_t q_desc = umma_desc_sw128(smem_u32(sQ)), k_desc = umma_desc_sw128(smem_u32(ring));
+    const uint64_t v_desc = prompt_desc_mn(smem_u32(ring), 128 * C::ROW);
+    constexpr uint64_t kTile = C::TILE >> 4;   // in descriptor units of 16 bytes
+    const auto scores = [&](int t, int slot) {   // S of tile t with the keys in `slot`
+      if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * 128 * C::ROW + (ks & 3) * 32;
-          umma_bf16(tmem + 128 * t, umma_desc_sw128(sQ_u + t * C::TILE + at), umma_desc_sw128(k_u + at), IDESC_S,
-                    ks != 0);
+          const uint64_t at = ((ks >> 2) * 128 * C::ROW + (ks & 3) * 32) >> 4;
+          umma_bf16(tmem + 128 * t, q_desc + t * kTile + at, k_desc + slot * kTile + at, IDESC_S, ks != 0);
         }
         umma_commit(&s_full[t]);
-      };
-      bool ok = n == 0 || (mbar_wait(q_full, 0, a.err, SITE_PROMPT_MMA) && wait_load(0));
-      if (ok && n > 0) {
-        for (int t = 0; t < 2; ++t)
-          if (steps[t] > 0) scores(t, 0);
-        umma_commit(&empty[0]);
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const bool more = j + 1 < n;
-        ok = wait_load(2 * j + 1);
-        // the next keys come while the softmax works
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j < steps[t]) {
-            if (!mbar_wait(&p_full[t], j & 1, a.err, SITE_PROMPT_MMA)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t v_u = ring_u + ((2 * j + 1) % C::SLOTS) * C::TILE;
+      __syncwarp();
+    };
+    const auto wait = [&](uint64_t* bar, int parity) {   // the same answer in every lane
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, a.err, SITE_PROMPT_MMA)) != 0;
+    };
+    bool ok = n == 0 || (wait(q_full, 0) && wait(&full[0], 0));
+    if (ok && n > 0) {
+      for (int t = 0; t < 2; ++t)
+        if (steps[t] > 0) scores(t, 0);
+      if (leader) umma_commit(&empty[0]);
+      __syncwarp();
+    }
+    int v_slot = 1, v_use = 0;   // slot of load 2 j + 1 and the parity of its use
+    for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      const int k_slot = v_slot + 1 == C::SLOTS ? 0 : v_slot + 1, k_use = k_slot == 0 ? v_use ^ 1 : v_use;   // load 2 j + 2
+      ok = wait(&full[v_slot], v_use);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_bf16_tmem_a(tmem + 256 + 128 * t, tmem + 128 * t + ks * 8,
-                               prompt_desc_mn(v_u + ks * 16 * C::ROW, 128 * C::ROW), IDESC_O, (j | ks) != 0);
-            if (j + 1 == steps[t]) umma_commit(&o_full[t]);
+      for (int t = 0; t < 2; ++t) {
+        if (!ok) break;
+        if (j < steps[t]) {
+          // the first half of the keys while the second is exponentiated
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(&p_full[2 * t + h], j & 1);
+            tc_fence_after();
+            if (ok && leader) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                umma_bf16_tmem_a(tmem + 256 + 128 * t, tmem + 128 * t + ks * 8,
+                                 v_desc + v_slot * kTile + ((ks * 16 * C::ROW) >> 4), IDESC_O, (j | ks) != 0);
+              if (h == 1 && j + 1 == steps[t]) umma_commit(&o_full[t]);
+            }
+            __syncwarp();
           }
-          if (t == 1) umma_commit(&empty[(2 * j + 1) % C::SLOTS]);
-          // S over the P just read: products of one thread run in order
-          if (more && j + 1 < steps[t]) {
-            if (!wait_load(2 * j + 2)) { ok = false; break; }
-            scores(t, j + 1);
-          }
-          if (t == 1 && more) umma_commit(&empty[(2 * j + 2) % C::SLOTS]);
         }
+        if (t == 1 && leader) umma_commit(&empty[v_slot]);
+        // S over the P just read: products of one thread run in order
+        if (ok && more && j + 1 < steps[t]) {
+          ok = wait(&full[k_slot], k_use);
+          if (ok) scores(t, k_slot);
+        }
+        if (t == 1 && more && leader) umma_commit(&empty[k_slot]);
       }
+      v_slot = k_slot + 1 == C::SLOTS ? 0 : k_slot + 1;
+      v_use = v_slot == 0 ? k_use ^ 1 : k_use;
+    }
+    if (leader) {
       umma_commit(mma_done);   // all issued products complete before TMEM is freed
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(mma_done, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
     }
+    __syncwarp();
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax and output, one row per thread
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
@@ -347,8 +416,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       for (int c = 0; c < 128; c += 8)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(r[c + 2 * k]), __uint_as_float(r[c + 2 * k + 1])));
-      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          mx[k] = max3_nan(mx[k], __uint_as_float(r[c + 2 * k]), __uint_as_float(r[c + 2 * k + 1]));
+      const float mn = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
       // a new reference only when the maximum has grown by 2^8 (or from nothing)
       const bool grow = mn > m && (m == -INFINITY || (mn - m) * a.scale_log2 > 8.f);
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -370,22 +439,10 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           }
         }
       }
+      // a NaN or +inf among the logits: the row is NaN, which the sum carries
+      if (!(mn < INFINITY)) l2[0] = pair(__int_as_float(0x7FFFFFFF), 0.f);
       const float mr = m == -INFINITY ? 0.f : m;
       const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), ms2 = pair(-mr * a.scale_log2, -mr * a.scale_log2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float x, y;
-          unpair(fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2), x, y);
-          x = fast_exp2(x);
-          y = fast_exp2(y);
-          l2[c & 1] = add2(l2[c & 1], pair(x, y));
-          p[c] = pack_bf16(x, y);
-        }
-        tmem_st32(s_col + 32 * h, p);
-      }
       if (masked) {
         // values of keys that some row of the tile does not attend: those
         // behind the sequence become zero, those inside it are looked over
@@ -406,10 +463,30 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint64_t x2 =
+              fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2);
+          float x, y;
+          if (c % 8 >= 8 - kPolyOf8) {
+            poly_exp2(x2, x, y);
+          } else {
+            unpair(x2, x, y);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+          }
+          l2[c & 1] = add2(l2[c & 1], pair(x, y));
+          p[c] = pack_bf16(x, y);
+        }
+        tmem_st32(s_col + 32 * h, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+      }
     }
     // whether any warp of the tile saw such a value (a barrier of its four warps)
     int any_odd = 0;

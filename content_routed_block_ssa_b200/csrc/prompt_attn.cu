@@ -28,9 +28,6 @@
 namespace ssa {
 namespace {
 
-// Of eight pairs of exponentials, how many go to the FMA pipe.
-constexpr int kPolyOf8 = 2;
-constexpr float kExp1 = 0.69312418f, kExp2 = 0.24024099f, kExp3 = 0.055906426f, kExp4 = 0.0095828529f;
 // Registers per thread of the softmax warps and of the others, traded at the
 // start: 2 * 208 + 88 = 3 * 168, what a block of 384 threads starts with.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -162,26 +159,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-// 2^x of a pair on the FMA pipe, x <= 2^7: x = n + f with |f| <= 1/2, 2^f by a
-// polynomial (least largest relative error on [-1/2, 1/2] with 2^0 = 1, fitted
-// for this kernel: 2^-18.4), n added to the exponent.  x below -127 (-inf of
-// masked keys) gives 0 exactly: n = -127 and f = 0 leave no bits.
-__device__ __forceinline__ void poly_exp2(uint64_t x2, float& x, float& y) {
-  unpair(x2, x, y);
-  x2 = pair(fmaxf(x, -127.f), fmaxf(y, -127.f));
-  const uint64_t t2 = add2(x2, pair(12582912.f, 12582912.f));   // 1.5 * 2^23: rounds to an integer
-  const uint64_t f2 = fma2(add2(t2, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x2);
-  uint64_t p2 = fma2(pair(kExp4, kExp4), f2, pair(kExp3, kExp3));
-  p2 = fma2(p2, f2, pair(kExp2, kExp2));
-  p2 = fma2(p2, f2, pair(kExp1, kExp1));
-  p2 = fma2(p2, f2, pair(1.f, 1.f));
-  float p, q, s, t;
-  unpair(p2, p, q);
-  unpair(t2, s, t);
-  x = __uint_as_float(__float_as_uint(p) + (__float_as_uint(s) << 23));
-  y = __uint_as_float(__float_as_uint(q) + (__float_as_uint(t) << 23));
-}
-
 __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
@@ -255,15 +232,34 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   }
   const int n = max(steps[0], steps[1]);
 
-  if (threadIdx.x == 0) {
+  // the loading lane sets up the barriers and starts the first loads while
+  // the others allocate tensor memory
+  const int loads = 2 * n;                              // K and V tiles in turn
+  const int early = min(loads, C::SLOTS);
+  const auto load = [&](int i) {
+    const int slot = i % C::SLOTS, row = u.k_row + (i / 2) * 128;
+    mbar_arrive_expect_tx(&full[slot], C::TILE);
+#pragma unroll
+    for (int hf = 0; hf < C::HALVES; ++hf)
+      tma_load_3d(ring + slot * C::TILE + hf * 128 * C::ROW, (i & 1) ? &tmV : &tmK, &full[slot], hf * 64, kvh, row);
+  };
+  if (warp == 8 && lane == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[2 * t], 4); mbar_init(&p_full[2 * t + 1], 4); mbar_init(&o_full[t], 1); }
     mbar_init(mma_done, 1);
     fence_barrier_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    if (n > 0) {
+      uint32_t bytes = 0;
+      for (int t = 0; t < 2; ++t) bytes += steps[t] > 0 ? static_cast<uint32_t>(a.qt * a.G * C::ROW * C::HALVES) : 0;
+      mbar_arrive_expect_tx(q_full, bytes);
+      for (int t = 0; t < 2; ++t)
+        if (steps[t] > 0)
+#pragma unroll
+          for (int hf = 0; hf < C::HALVES; ++hf)
+            tma_load_3d(sQ + t * C::TILE + hf * 128 * C::ROW, &tmQ, q_full, hf * 64, kvh * a.G, u.q_row + t * a.qt);
+      for (int i = 0; i < early; ++i) load(i);
+    }
   }
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
@@ -280,25 +276,12 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && n > 0) {
-      uint32_t bytes = 0;
-      for (int t = 0; t < 2; ++t) bytes += steps[t] > 0 ? static_cast<uint32_t>(a.qt * a.G * C::ROW * C::HALVES) : 0;
-      mbar_arrive_expect_tx(q_full, bytes);
-      for (int t = 0; t < 2; ++t)
-        if (steps[t] > 0)
-#pragma unroll
-          for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_load_3d(sQ + t * C::TILE + hf * 128 * C::ROW, &tmQ, q_full, hf * 64, kvh * a.G, u.q_row + t * a.qt);
-      int i = 0;
-      for (; i < 2 * n; ++i) {
-        const int slot = i % C::SLOTS, use = i / C::SLOTS;
-        if (use > 0 && !mbar_wait(&empty[slot], (use - 1) & 1, a.err, SITE_PROMPT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&full[slot], C::TILE);
-        const int row = u.k_row + (i / 2) * 128;
-#pragma unroll
-        for (int hf = 0; hf < C::HALVES; ++hf)
-          tma_load_3d(ring + slot * C::TILE + hf * 128 * C::ROW, (i & 1) ? &tmV : &tmK, &full[slot], hf * 64, kvh, row);
+      int i = early;
+      for (; i < loads; ++i) {
+        if (!mbar_wait(&empty[i % C::SLOTS], (i / C::SLOTS - 1) & 1, a.err, SITE_PROMPT_PRODUCER)) break;
+        load(i);
       }
-      if (i < 2 * n) {   // a wait gave up: let the copies in flight land
+      if (i < loads) {   // a wait gave up: let the copies in flight land
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(q_full, 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
         for (int k = max(0, i - C::SLOTS); k < i; ++k)
@@ -471,13 +454,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           const uint64_t x2 =
               fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2);
           float x, y;
-          if (c % 8 >= 8 - kPolyOf8) {
-            poly_exp2(x2, x, y);
-          } else {
-            unpair(x2, x, y);
-            x = fast_exp2(x);
-            y = fast_exp2(y);
-          }
+          unpair(x2, x, y);
+          x = fast_exp2(x);
+          y = fast_exp2(y);
           l2[c & 1] = add2(l2[c & 1], pair(x, y));
           p[c] = pack_bf16(x, y);
         }

@@ -4,8 +4,8 @@
 // A unit is up to 16 query rows that share a kv-head (new tokens x the G query
 // heads of the group; with selected blocks one token's G heads), and a unit's
 // keys are cut into `splits` runs, one block each, whose partial results a
-// second kernel joins.  Each of a block's four warps walks its own 32-key
-// pieces (every fourth of the run) with a ring of bulk copies of its own, so
+// second kernel joins.  Each of a block's three warps walks its own 32-key
+// pieces (every third of the run) with a ring of bulk copies of its own, so
 // no warp waits for another until the end.  The products are small against
 // the bytes (2 G flops per byte): the kernel is bound by reading codes, and
 // the instructions per code decide whether it keeps up:
@@ -39,8 +39,8 @@ namespace ssa {
 namespace {
 
 constexpr int kPiece = 32;     // keys per piece
-constexpr int kWarps = 4;
-constexpr int kBlocks = 3;     // blocks per SM (2 with 16 rows a unit, by registers)
+constexpr int kWarps = 3;
+constexpr int kBlocks = 4;     // blocks per SM (3 with 16 rows a unit, by registers)
 constexpr int kMaxEnt = 32 + 4032 / 64 + 2;   // selected blocks and window blocks
 constexpr int kSmCount = 148;
 
@@ -66,7 +66,7 @@ struct CacheShape {
   static constexpr int OROW = D + 4;   // floats per row of the join, skewed over the banks
   static constexpr int BARS = kWarps * RING;
   static constexpr int ENTS = BARS + kWarps * STAGES * 8;
-  static constexpr int SMEM = ENTS + (kMaxEnt + 1) * 4 + 12;
+  static constexpr int SMEM = ENTS + (kMaxEnt + 1) * 8;
   static_assert(kWarps * 16 * (OROW + 2) * 4 <= kWarps * RING, "the join fits the rings");
 };
 
@@ -138,7 +138,7 @@ struct Piece {
 
 // R: query rows of a unit in groups of eight.
 template <int D, bool SEL, int R>
-__global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_kernel(const CacheCfg a) {
+__global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_kernel(const CacheCfg a) {
   using C = CacheShape<D>;
   constexpr int MT = D / 16;    // output tiles of 16 dims
   constexpr int VW = D / 32;    // words of a value row per lane
@@ -146,13 +146,19 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::RING;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BARS) + warp * C::STAGES;
-  int32_t* ents = reinterpret_cast<int32_t*>(smem + C::ENTS);   // block | window flag in bit 30; then the count
+  int2* ents = reinterpret_cast<int2*>(smem + C::ENTS);   // (block | window flag in bit 30, page); then the count
 
   const int split = blockIdx.x % a.splits;
   const int unit = blockIdx.x / a.splits;
   const int kvh = unit % a.h_kv;
   const int tile = unit / a.h_kv % a.tiles;
   const int seq = unit / a.h_kv / a.tiles;
+  const int32_t* table = a.g.table + static_cast<int64_t>(seq) * a.max_pages;
+  int entry = -1, entry_page = -1;   // warp 0: this lane's block_idx entry and its page
+  if (SEL && warp == 0 && lane < a.topk) {
+    entry = __ldg(a.g.idx + ((static_cast<int64_t>(seq) * a.n_q + tile) * a.h_kv + kvh) * a.topk + lane);
+    if (entry >= 0 && entry < a.max_pages) entry_page = __ldg(table + entry);
+  }
   const int len = min(max(__ldg(a.g.kv_len + seq), 0), a.max_pages * a.page);
   // rows of the unit: row r is token (r0 + r) / G, head (r0 + r) % G
   const int r0 = SEL ? tile * a.G : tile * 8 * R;
@@ -168,7 +174,6 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
       pos[n][c] = r < n_rows ? first + (r0 + r) / a.G : -1;
     }
   const int ppb = a.page / kPiece;
-  const int32_t* table = a.g.table + static_cast<int64_t>(seq) * a.max_pages;
   const int wlo = SEL ? max(pos_hi - a.window + 1, 0) : 0;
 
   if (lane == 0)
@@ -178,14 +183,14 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
   int n_pieces;
   if (SEL) {
     if (warp == 0) {
-      // the used selected blocks, then the window's blocks outside them
+      // the used selected blocks, then the window's blocks outside them, with
+      // their pages.  The entries' pages are looked up before it is known which
+      // entries count: one load less in the chain to the first copy.
       int n = 0;
       if (pos_hi >= 0) {
-        const int32_t* row = a.g.idx + ((static_cast<int64_t>(seq) * a.n_q + tile) * a.h_kv + kvh) * a.topk;
         const int nvis = (pos_hi + 1) / a.page;
-        const int v = lane < a.topk ? __ldg(row + lane) : -1;
-        const bool inrange = v >= 0 && v < nvis;
-        int run = inrange ? v : -1;
+        const bool inrange = entry >= 0 && entry < nvis;
+        int run = inrange ? entry : -1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xFFFFFFFFu, run, o);
@@ -193,27 +198,28 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
         }
         int prev = __shfl_up_sync(0xFFFFFFFFu, run, 1);
         if (lane == 0) prev = -1;
-        const bool used = inrange && v > prev;
+        const bool used = inrange && entry > prev;
         const uint32_t um = __ballot_sync(0xFFFFFFFFu, used);
-        if (used) ents[__popc(um & ((1u << lane) - 1))] = v;
+        if (used) ents[__popc(um & ((1u << lane) - 1))] = make_int2(entry, entry_page);
         n = __popc(um);
-        const int skipped = __popc(__ballot_sync(0xFFFFFFFFu, lane < a.topk && v != -1 && !used));
+        const int skipped = __popc(__ballot_sync(0xFFFFFFFFu, lane < a.topk && entry != -1 && !used));
         if (lane == 0 && split == 0 && skipped && a.g.bad) atomicAdd(a.g.bad, skipped);
         __syncwarp();
         const int w1 = pos_hi / a.page;
         for (int b = wlo / a.page; b <= w1; b += 32) {
           const int blk = b + lane;
           bool add = blk <= w1;
-          for (int i = 0; i < __popc(um); ++i) add = add && ents[i] != blk;
+          const int pg = add ? __ldg(table + blk) : -1;
+          for (int i = 0; i < __popc(um); ++i) add = add && ents[i].x != blk;
           const uint32_t am = __ballot_sync(0xFFFFFFFFu, add);
-          if (add) ents[n + __popc(am & ((1u << lane) - 1))] = blk | 1 << 30;
+          if (add) ents[n + __popc(am & ((1u << lane) - 1))] = make_int2(blk | 1 << 30, pg);
           n += __popc(am);
         }
       }
-      if (lane == 0) ents[kMaxEnt] = n;
+      if (lane == 0) ents[kMaxEnt].x = n;
     }
     __syncthreads();
-    n_pieces = ents[kMaxEnt] * ppb;
+    n_pieces = ents[kMaxEnt].x * ppb;
   } else {
     __syncwarp();
     n_pieces = pos_hi >= 0 ? pos_hi / kPiece + 1 : 0;
@@ -229,14 +235,16 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
     p.ks = p.vs = 0.f;
     if (i < n_my) {
       const int c = c0 + warp + i * kWarps;
-      int blk = c / ppb;
+      int blk = c / ppb, page;
       if (SEL) {
-        const int e = ents[blk];
-        blk = e & ~(1 << 30);
-        p.lo = e >> 30 ? wlo : 0;
+        const int2 e = ents[blk];
+        blk = e.x & ~(1 << 30);
+        p.lo = e.x >> 30 ? wlo : 0;
+        page = e.y;
+      } else {
+        page = __ldg(table + blk);
       }
       p.key0 = blk * a.page + (c % ppb) * kPiece;
-      const int page = __ldg(table + blk);
       if (page >= 0 && page < a.n_pages) {
         p.page = page;
         const int64_t ph = static_cast<int64_t>(page) * a.h_kv + kvh;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 2) cache_attn_
       while (!mbar_try_wait(&full[i % C::STAGES], (i / C::STAGES) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
   }
 
-  // join the four warps: maxima and sums, then outputs, through the rings
+  // join the warps: maxima and sums, then outputs, through the rings
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -622,10 +630,20 @@ Split split_of(const ssa_cache_attn_params& p) {
     if (pieces > most) pieces = most;
   }
   // kBlocks blocks per SM run at a time: one wave of them when the units are
-  // fewer, else about three, so that ragged lengths even out; at least four
+  // few, else about four, so that ragged lengths even out; at least four
   // pieces per warp
   const int64_t room = kBlocks * kSmCount;
-  int64_t n = s.units < 1 ? 1 : s.units < room ? room / s.units : (3 * room + s.units - 1) / s.units;
+  int64_t n = s.units < 1 ? 1 : s.units * 8 < room ? room / s.units : (4 * room + s.units - 1) / s.units;
+  if (sel && s.units * 8 >= room) {
+    // units of one size: the split that costs least, a block's set-up and join
+    // counted as six pieces of a warp
+    int64_t best = 0, cost = INT64_MAX;
+    for (int64_t k = 1; k <= 8; ++k) {
+      const int64_t c = (s.units * k + room - 1) / room * (pieces + 6 * kWarps * k) * 840 / k;
+      if (c < cost) { cost = c; best = k; }
+    }
+    n = best;
+  }
   if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
   s.splits = static_cast<int>(n < 1 ? 1 : n);
   return s;

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "cache.cuh"
+#include "common.cuh"
 #include "kernels.h"
 #include "rope.cuh"
 
@@ -23,6 +24,9 @@ namespace ssa {
 namespace {
 
 constexpr int kKeep = 4;   // rows of a page per thread
+// Heads on their way or in use, in stages of 16 bytes (bf16) per row and thread.
+template <typename T>
+__host__ __device__ constexpr int page_stages() { return sizeof(T) == 2 ? 4 : 2; }
 
 struct AppendCfg {
   AppendArgs g;
@@ -37,16 +41,15 @@ struct AppendUnit {
   int32_t t0, n;       // new tokens (rows of K and V)
   int32_t slot0;       // slot of the first
   int32_t pos0;        // its position
-  int32_t page;        // -1: nothing to do
+  int32_t seq, place;  // its sequence and its page's place there
 };
 
-// All lanes of the warp get the unit; `count` (one caller per unit) adds what
-// is left out to the bad counter.
+// All lanes of the warp get the unit (n = 0: nothing to do); `count` (one
+// caller per unit) adds what is left out to the bad counter.
 template <int P>
 __device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t unit, bool count) {
   const int lane = threadIdx.x & 31;
   AppendUnit u;
-  u.page = -1;
   u.n = 0;
   const auto start = [&](int s) { return min(max(__ldg(a.g.new_start + s), 0), a.n_tokens); };
   int lo = 0, hi = a.n_seq;   // the sequence is in [lo, hi)
@@ -71,18 +74,21 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t un
   const int64_t p0 = max(static_cast<int64_t>(have), pi * P);
   const int64_t p1 = min(static_cast<int64_t>(have) + (a1 - a0), (pi + 1) * P);
   if (p1 <= p0) return u;
-  const int n = static_cast<int>(p1 - p0);
-  const int page = pi < a.max_pages ? __ldg(a.g.table + static_cast<int64_t>(lo) * a.max_pages + pi) : -1;
-  if (page < 0 || page >= a.n_pages) {
-    if (count && lane == 0 && a.g.bad) atomicAdd(a.g.bad, n);
-    return u;
-  }
-  u.n = n;
+  u.n = static_cast<int>(p1 - p0);
   u.t0 = a0 + static_cast<int>(p0 - have);
   u.slot0 = static_cast<int>(p0 - pi * P);
   u.pos0 = static_cast<int>(p0);
-  u.page = page;
+  u.seq = lo;
+  u.place = pi < a.max_pages ? static_cast<int>(pi) : -1;
   return u;
+}
+
+// The unit's page in the pool, -1 when it has none.
+__device__ __forceinline__ int unit_page(const AppendCfg& a, const AppendUnit& u, bool count) {
+  const int page = u.place >= 0 ? __ldg(a.g.table + static_cast<int64_t>(u.seq) * a.max_pages + u.place) : -1;
+  if (page >= 0 && page < a.n_pages) return page;
+  if (count && (threadIdx.x & 31) == 0 && a.g.bad) atomicAdd(a.g.bad, u.n);
+  return -1;
 }
 
 // The largest finite |x| * f of a row's elements and m (fmaxf leaves NaN out).
@@ -154,31 +160,61 @@ __device__ __forceinline__ int page_exponent(const AppendUnit& u, float amax, fl
   return e_new;
 }
 
-// Prompts: a block per (unit, K or V, run of kv-heads), the page's rows of a
-// head in registers, the next head's on their way.  The unit is looked up and
-// the angles are computed once for all the heads of the run.  (A block per
-// kv-head spent most of its life in the chain of index loads: 205 us for 64K
-// tokens of eight heads.)
+// A thread's eight dims of one row, global to its own place in shared memory.
+template <typename T>
+__device__ __forceinline__ void copy_row8(Run4<T>* a, Run4<T>* b, const T* row, const LaneDims& at) {
+  if (sizeof(T) == 2) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(a)), "l"(row + at.a) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(b)), "l"(row + at.b) : "memory");
+  } else {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(a)), "l"(row + at.a) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(b)), "l"(row + at.b) : "memory");
+  }
+}
+
+// Prompts: a block per (unit, K or V, run of kv-heads).  The unit is looked up
+// and the angles are computed once for all the heads of the run; a head's rows
+// stay in registers between the maximum and the rounding, and the next heads'
+// are on their way to shared memory, each thread's to its own place (no
+// barrier but the one of the maximum).  64K tokens of eight heads: a block per
+// kv-head took 205 us, most of it the chain of index loads; the next head
+// alone on its way 115 us, bound by the bytes in flight.
 template <typename T, int D, int P>
 __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1 : 2) append_page_kernel(const AppendCfg a) {
   constexpr int LPR = D / 8, KEEP = kKeep, THREADS = P * LPR / KEEP, ROWS = THREADS / LPR;
+  constexpr int STAGES = page_stages<T>();
   __shared__ float red[2][THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, sub = lane % LPR;
   const int row = threadIdx.x / LPR;
   const bool is_k = (blockIdx.x & 1) == 0;   // keys take longer: the two kinds take turns
   const int item = static_cast<int>(blockIdx.x >> 1);
   const int h0 = item % a.runs * a.per_run, h1 = min(h0 + a.per_run, a.h_kv);
-  const AppendUnit u = append_unit<P>(a, item / a.runs, h0 == 0 && is_k && warp == 0);
-  if (u.page < 0) return;
+  const bool count = h0 == 0 && is_k && warp == 0;
+  const AppendUnit u = append_unit<P>(a, item / a.runs, count);
+  if (u.n == 0) return;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const LaneDims at(sub, is_k ? a.rot : 0, a.layout);
   const T* src[KEEP];
-  Row8<T> r[KEEP];
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) {   // rows past the last repeat it: the same maximum
-    src[k] = static_cast<const T*>(is_k ? a.g.K : a.g.V) + (u.t0 + min(row + k * ROWS, u.n - 1)) * stride +
-             static_cast<int64_t>(h0) * D;
-    r[k].load(src[k], at);
+  for (int k = 0; k < KEEP; ++k)   // rows past the last repeat it: the same maximum
+    src[k] = static_cast<const T*>(is_k ? a.g.K : a.g.V) + (u.t0 + min(row + k * ROWS, u.n - 1)) * stride;
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  Run4<T>* ring = reinterpret_cast<Run4<T>*>(ring_raw) + threadIdx.x;   // [stages][KEEP][2][THREADS]
+  const auto fetch = [&](int h) {   // a group per head, empty past the last
+    if (h < h1) {
+      Run4<T>* to = ring + (h % STAGES) * (KEEP * 2 * THREADS);
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k)
+        copy_row8(to + 2 * k * THREADS, to + (2 * k + 1) * THREADS, src[k] + static_cast<int64_t>(h) * D, at);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(h0 + s);
+  const int page = unit_page(a, u, count);   // looked up while the rows are on their way
+  if (page < 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
   }
   float w[8];
   lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
@@ -190,24 +226,22 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1
     for (int k = 0; k < KEEP; ++k)
       angles[k].set<sizeof(T) == 4>(at, phase, u.pos0 + min(row + k * ROWS, u.n - 1), a.mscale);
   }
-  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + h0;
+  const int64_t ph = static_cast<int64_t>(page) * a.h_kv + h0;
   uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
   float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
   for (int h = h0; h < h1; ++h, codes += P * D, ++scale) {
     const float old = u.slot0 > 0 ? *scale : 0.f;
+    fetch(h + STAGES - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    const Run4<T>* from = ring + (h % STAGES) * (KEEP * 2 * THREADS);
     float x[KEEP][8], f[KEEP];
     float amax = 0.f;
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
-      f[k] = append_row<T, LPR>(a, is_k, r[k], at, w, angles[k], x[k]);
+      const Row8<T> r{from[2 * k * THREADS], from[(2 * k + 1) * THREADS]};
+      f[k] = append_row<T, LPR>(a, is_k, r, at, w, angles[k], x[k]);
       amax = finite_amax(x[k], f[k], amax);
     }
-    if (h + 1 < h1)
-#pragma unroll
-      for (int k = 0; k < KEEP; ++k) {
-        src[k] += D;
-        r[k].load(src[k], at);
-      }
     amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
     if (lane == 0) red[h & 1][warp] = amax;
     __syncthreads();   // the maxima are there, and every thread has the old scale
@@ -236,7 +270,9 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   const bool is_k = hk < a.h_kv;
   const int head = is_k ? hk : hk - a.h_kv;
   const AppendUnit u = append_unit<P>(a, unit, hk == 0);
-  if (u.page < 0) return;
+  if (u.n == 0) return;
+  const int page = unit_page(a, u, hk == 0);
+  if (page < 0) return;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const T* src = static_cast<const T*>(is_k ? a.g.K : a.g.V) + static_cast<int64_t>(u.t0) * stride +
                  static_cast<int64_t>(head) * D;
@@ -260,7 +296,7 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
     amax = finite_amax(x, f, amax);
   }
   amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
-  const int64_t ph = static_cast<int64_t>(u.page) * a.h_kv + head;
+  const int64_t ph = static_cast<int64_t>(page) * a.h_kv + head;
   uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
   float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
   const int e = page_exponent<D>(u, amax, u.slot0 > 0 ? *scale : 0.f, codes, lane, 32);
@@ -290,7 +326,11 @@ cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
     a.runs = (a.h_kv + a.per_run - 1) / a.per_run;
     const int64_t grid = units * a.runs * 2;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    append_page_kernel<T, D, P><<<static_cast<unsigned>(grid), P * D / 8 / kKeep, 0, c.stream>>>(a);
+    constexpr int kThreads = P * D / 8 / kKeep, kSmem = page_stages<T>() * kKeep * kThreads * 8 * sizeof(T);
+    const cudaError_t e =
+        cudaFuncSetAttribute(append_page_kernel<T, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    append_page_kernel<T, D, P><<<static_cast<unsigned>(grid), kThreads, kSmem, c.stream>>>(a);
   }
   note_launch();
   return cudaGetLastError();

@@ -37,6 +37,7 @@ enum WaitSite : uint32_t {
   SITE_WIN_MMA = 0x502,
   SITE_WIN_SOFTMAX = 0x503,
   SITE_WIN_SMEM = 0x504,       // the aligned shared-memory layout did not fit its allocation
+  SITE_ROPE_FULL = 0x5F1,      // rotation: a piece of a token's heads
   SITE_CACHE_FULL = 0x601,     // attention over the paged cache: a piece of a page
   SITE_PROMPT_PRODUCER = 0x611,   // attention over packed prompts
   SITE_PROMPT_MMA = 0x612,
@@ -144,6 +145,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05

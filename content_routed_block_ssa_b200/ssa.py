@@ -437,23 +437,26 @@ def _addresses(dev, specs, tensors):
     """Addresses of a serving operator's operands, each checked against its
     (name, type, shape, strides or None for dense) and the current device."""
     out = []
-    for spec, t in zip(specs, tensors):
+    add = out.append
+    for (name, dtype, shape, strides), t in zip(specs, tensors):
         if t is None:
-            out.append(None)
-        elif t.dtype is spec[1] and t.shape == spec[2] and t.get_device() == dev and \
-                (t.is_contiguous() if spec[3] is None else t.stride() == spec[3]):
-            out.append(t.data_ptr())
+            add(None)
+        elif t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+                (t.is_contiguous() if strides is None else t.stride() == strides):
+            add(t.data_ptr())
         else:
-            out.append(_refuse(spec, t, dev))
+            add(_refuse((name, dtype, shape, strides), t, dev))
     return out
 
 
 def _here(stream):
     """(current device, stream address); without a GPU a device that no
     tensor is on."""
-    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
-        return -2, 0
-    dev = torch.cuda.current_device()
+    if not torch.cuda.is_initialized():
+        if not torch.cuda.is_available():
+            return -2, 0
+        torch.cuda.init()
+    dev = torch._C._cuda_getDevice()
     return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 

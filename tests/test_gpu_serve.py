@@ -115,6 +115,42 @@ def test_rope_many_tokens_and_far_positions():
     assert (np.abs(f64(qo) - ref) <= U["f32"] * np.abs(ref) + (FUZZ["f32"] + 2.0 ** -20) * big).all()
 
 
+@pytest.mark.parametrize("dtype,d,rot,layout,hq,hkv,T", [
+    ("bf16", 128, 128, "half", 32, 8, 2600), ("bf16", 64, 32, "pairs", 33, 1, 3000), ("f32", 128, 96, "half", 9, 3, 3001),
+    ("f32", 64, 64, "pairs", 5, 17, 2500), ("bf16", 128, 0, "half", 1, 1, 4000)])
+def test_rope_of_many_tokens(dtype, d, rot, layout, hq, hkv, T):
+    """Enough tokens for the streaming kernel, ragged numbers of heads per
+    piece, in place too: sampled tokens against the oracle, every token
+    against the same tokens in small calls (two roundings apart at most)."""
+    r = rng_of("stream", dtype, d, hq)
+    x = dev(r.normal(size=(T, hq + hkv + 1, d)), TD[dtype])
+    q, k = x[:, :hq], x[:, hq:hq + hkv]
+    qw, kw = dev(r.normal(size=d), torch.float32), dev(1 + r.normal(size=d), torch.float32)
+    f = ssa.rope_frequencies(max(rot, 2))[0][:rot // 2]
+    pos = r.integers(-100, 1 << 20, size=T)
+    pd, fd = dev(pos, torch.int32), f.cuda()
+    small = []
+    for i in range(0, T, 100):
+        n = min(100, T - i)
+        p = ssa.make_rope_params(n, hq, hkv, d, rot, layout, dtype, True, 1e-6, 1.1, q_stride=x.stride(0), k_stride=x.stride(0))
+        o = torch.empty(n, hq, d, device="cuda", dtype=TD[dtype]), torch.empty(n, hkv, d, device="cuda", dtype=TD[dtype])
+        ssa.ssa_qk_rope(p, q[i:i + n], k[i:i + n], qw, kw, fd, pd[i:i + n], *o)
+        small.append(o)
+    small = [torch.cat(s) for s in zip(*small)]
+    before = x.clone()
+    s = x.stride(0)
+    p = ssa.make_rope_params(T, hq, hkv, d, rot, layout, dtype, True, 1e-6, 1.1, s, s, s, s)
+    ssa.ssa_qk_rope(p, q, k, qw, kw, fd, pd, q, k)
+    ok()
+    assert torch.equal(x[:, hq + hkv:], before[:, hq + hkv:])
+    at = np.unique(np.concatenate([r.integers(0, T, 60), [0, T - 1]]))
+    for got, was, w, sm in ((q, before[:, :hq], qw, small[0]), (k, before[:, hq:hq + hkv], kw, small[1])):
+        check_rope(got[at], f64(was[at]), f64(w), f.numpy(), pos[at], layout, 1.1, True, 1e-6, dtype)
+        a, b = got.double(), sm.double()
+        big = b.abs().amax(-1, keepdim=True)
+        assert ((a - b).abs() <= 2 * U[dtype] * b.abs() + 2 * FUZZ[dtype] * big).all()
+
+
 def test_rope_leaves_unrotated_infinities_and_keeps_heads_apart():
     x = torch.ones(2, 3, 128, device="cuda")
     x[0, 0, 100] = math.inf

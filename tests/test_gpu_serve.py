@@ -433,6 +433,88 @@ def test_cache_attention_over_selected_blocks(d, page, window, h_kv, G, n_q, top
     assert int(bad) == skipped
 
 
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128)])
+def test_cache_attention_many_rows_over_a_split_axis(d, page):
+    """More rows per kv-head than one unit holds, and a split axis; sixteen
+    query heads per kv-head over selected blocks."""
+    r = rng_of("rows", d)
+    lens = [2100, 3, 1777]
+    table, codes, scale, q, _ = cache_case(r, lens, 5, 1, 8, d, page)
+    o, lse, p = run_cache(q, lens, table, codes, scale, page)
+    assert ssa.ssa_cache_attn_workspace_size(p) > 0
+    check_cache(o, lse, q, lens, table, codes, scale, page)
+    table, codes, scale, q, idx = cache_case(r, lens, 2, 1, 16, d, page, 8)
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, idx, 150)
+    check_cache(o, lse, q, lens, table, codes, scale, page, idx, 150)
+
+
+def test_cache_pool_past_32_bit_offsets():
+    """A pool of more than 2^32 bytes: appended to and attended at its end."""
+    page, d, h = 128, 128, 8
+    n_pages = (1 << 32) // (page * d * h) + 40
+    kc = torch.zeros(n_pages, h, page, d, dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    ks, vs = torch.ones(n_pages, h, device="cuda"), torch.ones(n_pages, h, device="cuda")
+    r = rng_of("far")
+    table = np.array([[n_pages - 1, 3, n_pages - 17]])
+    T = 300
+    x = dev(r.normal(size=(T, 2 * h, d)), torch.bfloat16)
+    p = ssa.make_append_params(T, 1, 3, n_pages, page, h, d, 0, norm=False, k_stride=x.stride(0), v_stride=x.stride(0))
+    td = dev(table, torch.int32)
+    ssa.ssa_cache_append(p, x[:, :h], x[:, h:], None, None, dev([0, T], torch.int32), dev([0], torch.int32), td, kc, vc, ks, vs)
+    q = dev(r.normal(size=(1, 1, 16, d)), torch.bfloat16)
+    pa = ssa.make_cache_attn_params(1, 1, 3, n_pages, page, 16, h, d)
+    o, lse = torch.empty_like(q), torch.empty(1, 1, 16, device="cuda")
+    ws = ssa.byte_buffer(ssa.ssa_cache_attn_workspace_size(pa))
+    # the codes may come as float8, the same memory
+    ssa.ssa_cache_attn(pa, q, td, dev([T], torch.int32), kc.view(E4M3), vc.view(E4M3), ks, vs, None, o, lse, ws=ws)
+    ok()
+    at = td[0].long()
+    codes, scale = np.stack([kc[at].cpu().numpy(), vc[at].cpu().numpy()]), np.stack([f64(ks[at]), f64(vs[at])])
+    check_cache(o, lse, q, [T], np.array([[0, 1, 2]]), codes, scale, page)
+    rc, rs, _ = S.append(f64(x[:, :h]), [0, T], [0], [[0, 1, 2]], page, np.zeros_like(codes[0]), np.ones_like(scale[0]))
+    assert np.array_equal(codes[0], rc) and np.array_equal(scale[0], rs)
+    used = torch.zeros(n_pages, dtype=torch.bool, device="cuda")
+    used[at] = True
+    assert not kc[~used].any() and (ks[~used] == 1).all()
+
+
+def test_tokens_far_apart():
+    """Tokens 2^27 elements apart: offsets past 2^31 elements in every operator
+    that takes strided tokens, also with a gap before the first sequence."""
+    T, h, d, step = 40, 2, 64, 1 << 27
+    buf = torch.empty(T * step, dtype=torch.bfloat16, device="cuda")
+    r = rng_of("apart")
+    x = buf.as_strided((T, 4 * h, d), (step, d, 1))
+    x.copy_(dev(r.normal(size=(T, 4 * h, d)), torch.bfloat16))
+    near = x.contiguous()
+    q, k, v, o = (x[:, i * h:(i + 1) * h] for i in range(4))
+    nq, nk, nv, _ = (near[:, i * h:(i + 1) * h] for i in range(4))
+    qs = [3, 20, 40]
+    pp = ssa.make_prompt_params(2, T, T, h, h, d, step, step, step, step)
+    st = dev(qs, torch.int32)
+    ssa.ssa_prompt_attn(pp, q, k, v, st, st, o)
+    ok()
+    on, _ = run_prompt(nq, nk, nv, qs, qs)
+    assert torch.equal(o[3:], on[3:]) and torch.equal(o[:3], near[:3, 3 * h:]) and (on[:3] == 7).all()
+    f, pos = ssa.rope_frequencies(d)[0].cuda(), dev(np.arange(T), torch.int32)
+    want = torch.empty(T, h, d, dtype=torch.bfloat16, device="cuda"), torch.empty(T, h, d, dtype=torch.bfloat16, device="cuda")
+    s = near.stride(0)
+    ssa.ssa_qk_rope(ssa.make_rope_params(T, h, h, d, q_stride=s, k_stride=s), nq, nk, None, None, f, pos, *want)
+    for n in (2, 40):                                           # the decode kernel and the page kernel
+        table, codes, scale = np.array([[2, 0], [1, 3]]), *pool(r, 4, h, 64, d)
+        two = []
+        for a, b, sa in ((k, v, step), (nk, nv, s)):
+            ap = ssa.make_append_params(n, 2, 2, 4, 64, h, d, k_stride=sa, v_stride=sa)
+            (kc, vc, ks, vs), bad = run_append(ap, a[T - n:], b[T - n:], None, f, np.array([1, n - n // 2, n]), np.array([60, 0]), table, codes, scale)
+            two.append((kc, vc, ks, vs))
+        assert all(torch.equal(a, b) for a, b in zip(*two))
+    ssa.ssa_qk_rope(ssa.make_rope_params(T, h, h, d, q_stride=step, k_stride=step, q_out_stride=step, k_out_stride=step),
+                    q, k, None, None, f, pos, q, k)
+    ok()
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_cache_attention_equals_the_layer_on_the_same_keys():
     """With values that the codes hold exactly, decode over the cache is the
     layer's decode (route, then attend) over dense keys: same selection, same
@@ -635,6 +717,13 @@ def test_prompt_ignores_what_a_row_does_not_attend():
     assert torch.equal(o[~o.isnan()], clean[~o.isnan()])
 
 
+def test_prompt_without_any_keys():
+    q = torch.ones(5, 8, 64, device="cuda", dtype=torch.bfloat16)
+    kv = torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16)
+    o, lse = run_prompt(q, kv, kv, [0, 4], [0, 0])
+    assert not o[:4].any() and (lse[:4] == -math.inf).all() and (o[4] == 7).all() and (lse[4] == 7).all()
+
+
 def test_prompt_offsets_that_do_not_fit():
     """Decreasing or out-of-range offsets read and write nothing outside the
     operands; rows that no sequence covers stay as they were."""
@@ -793,6 +882,62 @@ def test_prompt_then_decode_agree():
         g.replay()
         ok()
         assert torch.equal(out, o) and torch.equal(ol, lse)
+
+
+FIRST_CALL = """
+import torch
+from content_routed_block_ssa_b200 import ssa
+dev = dict(device="cuda")
+q = torch.randn(4, 8, 64, **dev).bfloat16()
+k = torch.randn(4, 2, 64, **dev).bfloat16()
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, **dev)
+o, qo, ko = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(k)
+kc, vc = torch.zeros(2, 2, 64, 64, dtype=torch.uint8, **dev), torch.zeros(2, 2, 64, 64, dtype=torch.uint8, **dev)
+ks, vs = torch.zeros(2, 2, **dev), torch.zeros(2, 2, **dev)
+f, cu, pos, table, have = ssa.rope_frequencies(64)[0].cuda(), i32(0, 4), i32(0, 1, 2, 3), i32(0, 1).view(1, 2), i32(0)
+oc, ln = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16, **dev), i32(4)
+def step():
+    ssa.ssa_qk_rope(ssa.make_rope_params(4, 8, 2, 64), q, k, None, None, f, pos, qo, ko)
+    ssa.ssa_cache_append(ssa.make_append_params(4, 1, 2, 2, 64, 2, 64), k, k, None, f, cu, have, table, kc, vc, ks, vs)
+    ssa.ssa_cache_attn(ssa.make_cache_attn_params(1, 1, 2, 2, 64, 8, 2, 64), qo[3:].view(1, 1, 8, 64), table, ln, kc, vc, ks, vs, None, oc)
+    ssa.ssa_prompt_attn(ssa.make_prompt_params(1, 4, 4, 8, 2, 64), qo, ko, k, cu, cu, o)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+a, b = o.clone(), oc.clone()
+step()
+torch.cuda.synchronize()
+assert a.any() and b.any() and torch.equal(a, o) and torch.equal(b, oc) and ssa.ssa_device_error() == 0
+print("captured first")
+"""
+
+
+def test_the_first_call_may_be_captured():
+    import subprocess
+    import sys
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    r = rng_of("two")
+    lens, page = [3000, 2500], 64
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 2, 4, 128, page)
+    ref, ref_l, p = run_cache(q, lens, table, codes, scale, page)
+    args = (p, q, dev(table, torch.int32), dev(lens, torch.int32), dev(codes[0]), dev(codes[1]),
+            dev(scale[0], torch.float32), dev(scale[1], torch.float32), None)
+    n = ssa.ssa_cache_attn_workspace_size(p)
+    outs = [(torch.zeros_like(q), torch.zeros_like(ref_l), ssa.byte_buffer(n), torch.cuda.Stream()) for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o, l, ws, st in outs:
+            ssa.ssa_cache_attn(*args, o, l, None, ws, st)
+    ok()
+    assert all(torch.equal(o, ref) and torch.equal(l, ref_l) for o, l, _, _ in outs)
 
 
 def test_results_do_not_depend_on_the_run():

@@ -28,22 +28,29 @@
 namespace ssa {
 namespace {
 
-// Registers per thread of the softmax warps and of the others, traded at the
-// start: 2 * 208 + 88 = 3 * 168, what a block of 384 threads starts with.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-
-template <int D>
+// TILES: tensor-core tiles per block.  Two share their keys' loads and take
+// turns; one, with half of an SM for its block, gives twice the blocks where
+// there are few (see launch_prompt_attn).
+template <int D, int TILES>
 struct PromptShape {
   static constexpr int ROW = 128;                     // bytes of a 64-dim swizzled row
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = 128 * ROW * HALVES;     // 128 rows (queries x heads, or keys)
-  static constexpr int SLOTS = D == 128 ? 5 : 8;      // ring of K and V tiles
-  static constexpr int BARS = 2 * TILE + SLOTS * TILE;
-  static constexpr int NBAR = 1 + 2 * SLOTS + 2 + 4 + 2 + 1;
+  static constexpr int SLOTS = TILES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);   // ring of K and V tiles
+  static constexpr int BARS = TILES * TILE + SLOTS * TILE;
+  static constexpr int NBAR = 1 + 2 * SLOTS + TILES + 2 * TILES + TILES + 1;
   static constexpr int USED = BARS + NBAR * 8 + 16;
   static constexpr int SMEM = USED + 1024 < 232448 ? USED + 1024 : 232448;
-  static constexpr int THREADS = 384;                 // 2 x 4 softmax warps; loads, products and two idle
+  static constexpr int LOADER = 4 * TILES, ISSUER = LOADER + 1;   // warps: 4 softmax warps per tile, loads, products
+  static constexpr int THREADS = (LOADER + 4) * 32;               // and two idle ones that hand over registers
+  static constexpr int BLOCKS = TILES == 2 ? 1 : 2;               // per SM
+  static constexpr int COLS = 256 * TILES;                        // S of tile t at 128 t, O at 128 (TILES + t)
+  // Registers per thread of the softmax warps and of the others, traded at the
+  // start: 2 * 208 + 88 = 3 * 168, what a block of 384 threads starts with, and
+  // 208 + 48 = 2 * 128 for one of 256 threads at two per SM.
+  static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = TILES == 2 ? 88 : 48;
   static_assert(USED <= 232448, "shared memory");
+  static_assert(BLOCKS * (SMEM + 1024) <= 233472, "blocks per SM");
 };
 
 struct PromptArgs {
@@ -64,8 +71,8 @@ struct PromptUnit {
 };
 
 // Warp-collective.
-__device__ __forceinline__ PromptUnit prompt_unit(const PromptArgs& a, int unit) {
-  const int lane = threadIdx.x & 31, rows = 2 * a.qt;
+__device__ __forceinline__ PromptUnit prompt_unit(const PromptArgs& a, int rows, int unit) {
+  const int lane = threadIdx.x & 31;
   PromptUnit u{};
   const auto start = [&](int s) { return min(max(__ldg(a.q_start + s), 0), a.n_q); };
   int lo = 0, hi = a.n_seq;
@@ -193,15 +200,15 @@ __device__ void plain_row(const PromptArgs& a, const __nv_bfloat16* q, const Pro
   for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16(o[e] * inv_l);
 }
 
-template <int D>
-__global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
+template <int D, int TILES>
+__global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D, TILES>::BLOCKS)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PromptArgs a) {
-  using C = PromptShape<D>;
+  using C = PromptShape<D, TILES>;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0);   // known to be uniform
   const int lane = threadIdx.x & 31;
   const int kvh = blockIdx.x % a.h_kv;
-  const PromptUnit u = prompt_unit(a, a.n_units - 1 - static_cast<int>(blockIdx.x / a.h_kv));
+  const PromptUnit u = prompt_unit(a, TILES * a.qt, a.n_units - 1 - static_cast<int>(blockIdx.x / a.h_kv));
   if (!u.any) return;   // the same for every warp
 
   extern __shared__ uint8_t smem_raw[];
@@ -210,27 +217,30 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     if (threadIdx.x == 0) atomicCAS(a.err, 0u, static_cast<uint32_t>(SITE_PROMPT_SMEM));
     return;
   }
-  uint8_t* sQ = smem;                   // [2 tiles][halves][128 rows][128 B]
-  uint8_t* ring = smem + 2 * C::TILE;   // [slots][halves][128 keys][128 B]: K0 V0 K1 V1 ...
+  uint8_t* sQ = smem;                       // [tiles][halves][128 rows][128 B]
+  uint8_t* ring = smem + TILES * C::TILE;   // [slots][halves][128 keys][128 B]: K0 V0 K1 V1 ...
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
   uint64_t* q_full = bars;
   uint64_t* full = bars + 1;
   uint64_t* empty = full + C::SLOTS;
-  uint64_t* s_full = empty + C::SLOTS;   // [2 tiles]
-  uint64_t* p_full = s_full + 2;         // [2 tiles][2 halves of the step's keys]
-  uint64_t* o_full = p_full + 4;         // the tile's last product is done
-  uint64_t* mma_done = o_full + 2;
+  uint64_t* s_full = empty + C::SLOTS;     // [tiles]
+  uint64_t* p_full = s_full + TILES;       // [tiles][2 halves of the step's keys]
+  uint64_t* o_full = p_full + 2 * TILES;   // [tiles] the tile's last product is done
+  uint64_t* mma_done = o_full + TILES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
 
-  // steps of each tile: keys 0 .. position of its last row
+  // steps of each tile: keys 0 .. position of its last row; a last step that
+  // needs no more than half of its 128 keys leaves out the rest
   const int off = u.kv_len - u.q_len;
-  int steps[2];
+  int steps[TILES], n = 0;
+  bool short_last[TILES];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int q_first = u.q0 + t * a.qt, q_last = min(q_first + a.qt, u.q_len) - 1;
-    steps[t] = q_first < u.q_len && q_last + off >= 0 ? (q_last + off) / 128 + 1 : 0;
+  for (int t = 0; t < TILES; ++t) {
+    const int q_first = u.q0 + t * a.qt, last = min(q_first + a.qt, u.q_len) - 1 + off;
+    steps[t] = q_first < u.q_len && last >= 0 ? last / 128 + 1 : 0;
+    short_last[t] = steps[t] > 0 && last % 128 < 64;
+    n = max(n, steps[t]);
   }
-  const int n = max(steps[0], steps[1]);
 
   // the loading lane sets up the barriers and starts the first loads while
   // the others allocate tensor memory
@@ -243,17 +253,22 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     for (int hf = 0; hf < C::HALVES; ++hf)
       tma_load_3d(ring + slot * C::TILE + hf * 128 * C::ROW, (i & 1) ? &tmV : &tmK, &full[slot], hf * 64, kvh, row);
   };
-  if (warp == 8 && lane == 0) {
+  if (warp == C::LOADER && lane == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < C::SLOTS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[2 * t], 4); mbar_init(&p_full[2 * t + 1], 4); mbar_init(&o_full[t], 1); }
+    for (int t = 0; t < TILES; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
+      mbar_init(&o_full[t], 1);
+    }
     mbar_init(mma_done, 1);
     fence_barrier_init();
     if (n > 0) {
       uint32_t bytes = 0;
-      for (int t = 0; t < 2; ++t) bytes += steps[t] > 0 ? static_cast<uint32_t>(a.qt * a.G * C::ROW * C::HALVES) : 0;
+      for (int t = 0; t < TILES; ++t) bytes += steps[t] > 0 ? static_cast<uint32_t>(a.qt * a.G * C::ROW * C::HALVES) : 0;
       mbar_arrive_expect_tx(q_full, bytes);
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < TILES; ++t)
         if (steps[t] > 0)
 #pragma unroll
           for (int hf = 0; hf < C::HALVES; ++hf)
@@ -261,19 +276,19 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       for (int i = 0; i < early; ++i) load(i);
     }
   }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
+  if (warp == C::ISSUER) {
+    tmem_alloc(tmem_slot, C::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;   // S of tile t at 128 t, O at 256 + 128 t
+  const uint32_t tmem = *tmem_slot, tmem_o = tmem + 128 * TILES;   // S and O of tile t at 128 t of each
 
-  if (warp >= 8) {
-    // this warpgroup hands registers to the two softmax warpgroups
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 8) {
+  if (warp >= C::LOADER) {
+    // this warpgroup hands registers to the softmax warpgroups
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+  if (warp == C::LOADER) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && n > 0) {
       int i = early;
@@ -288,24 +303,25 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           while (!mbar_try_wait(&full[k % C::SLOTS], (k / C::SLOTS) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ products
     // The whole warp runs the loop, so that descriptors and counters stay in
     // uniform registers, and one lane issues: with one lane running all of it
     // the issue, not the tensor core, set the pace (about 95 clocks per
     // product of 64).
     const bool leader = elect_one();
-    constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 128);
+    constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 128), IDESC_S64 = umma_idesc_bf16(128, 64);
     constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);   // V is MN-major
     const uint64_t q_desc = umma_desc_sw128(smem_u32(sQ)), k_desc = umma_desc_sw128(smem_u32(ring));
     const uint64_t v_desc = prompt_desc_mn(smem_u32(ring), 128 * C::ROW);
     constexpr uint64_t kTile = C::TILE >> 4;   // in descriptor units of 16 bytes
-    const auto scores = [&](int t, int slot) {   // S of tile t with the keys in `slot`
+    const auto scores = [&](int t, int j, int slot) {   // S of tile t, step j, with the keys in `slot`
+      const uint32_t idesc = short_last[t] && j + 1 == steps[t] ? IDESC_S64 : IDESC_S;
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t at = ((ks >> 2) * 128 * C::ROW + (ks & 3) * 32) >> 4;
-          umma_bf16(tmem + 128 * t, q_desc + t * kTile + at, k_desc + slot * kTile + at, IDESC_S, ks != 0);
+          umma_bf16(tmem + 128 * t, q_desc + t * kTile + at, k_desc + slot * kTile + at, idesc, ks != 0);
         }
         umma_commit(&s_full[t]);
       }
@@ -316,8 +332,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     };
     bool ok = n == 0 || (wait(q_full, 0) && wait(&full[0], 0));
     if (ok && n > 0) {
-      for (int t = 0; t < 2; ++t)
-        if (steps[t] > 0) scores(t, 0);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+        if (steps[t] > 0) scores(t, 0, 0);
       if (leader) umma_commit(&empty[0]);
       __syncwarp();
     }
@@ -327,8 +344,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       const int k_slot = v_slot + 1 == C::SLOTS ? 0 : v_slot + 1, k_use = k_slot == 0 ? v_use ^ 1 : v_use;   // load 2 j + 2
       ok = wait(&full[v_slot], v_use);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TILES; ++t) {
         if (!ok) break;
+        const bool brief = short_last[t] && j + 1 == steps[t];
         if (j < steps[t]) {
           // the first half of the keys while the second is exponentiated
 #pragma unroll
@@ -336,22 +354,23 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
             ok = ok && wait(&p_full[2 * t + h], j & 1);
             tc_fence_after();
             if (ok && leader) {
+              if (h == 0 || !brief)
 #pragma unroll
-              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                umma_bf16_tmem_a(tmem + 256 + 128 * t, tmem + 128 * t + ks * 8,
-                                 v_desc + v_slot * kTile + ((ks * 16 * C::ROW) >> 4), IDESC_O, (j | ks) != 0);
+                for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                  umma_bf16_tmem_a(tmem_o + 128 * t, tmem + 128 * t + ks * 8,
+                                   v_desc + v_slot * kTile + ((ks * 16 * C::ROW) >> 4), IDESC_O, (j | ks) != 0);
               if (h == 1 && j + 1 == steps[t]) umma_commit(&o_full[t]);
             }
             __syncwarp();
           }
         }
-        if (t == 1 && leader) umma_commit(&empty[v_slot]);
+        if (t == TILES - 1 && leader) umma_commit(&empty[v_slot]);
         // S over the P just read: products of one thread run in order
         if (ok && more && j + 1 < steps[t]) {
           ok = wait(&full[k_slot], k_use);
-          if (ok) scores(t, k_slot);
+          if (ok) scores(t, j + 1, k_slot);
         }
-        if (t == 1 && more && leader) umma_commit(&empty[k_slot]);
+        if (t == TILES - 1 && more && leader) umma_commit(&empty[k_slot]);
       }
       v_slot = k_slot + 1 == C::SLOTS ? 0 : k_slot + 1;
       v_use = v_slot == 0 ? k_use ^ 1 : k_use;
@@ -364,12 +383,14 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     // ------------------------------------------------------------ softmax and output, one row per thread
-    const int t = warp >> 2;
+    const int t = TILES == 2 ? warp >> 2 : 0;
+    const int my_steps = steps[t];
+    const bool my_short = short_last[t];
     const int row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lanes + 128 * t, o_col = tmem + lanes + 256 + 128 * t;
+    const uint32_t s_col = tmem + lanes + 128 * t, o_col = tmem_o + lanes + 128 * t;
     const int qi = u.q0 + t * a.qt + row / a.G;             // query of the row within its sequence
     const bool valid = row < a.qt * a.G && qi < u.q_len;
     const int pos = valid ? qi + off : -1;
@@ -378,13 +399,15 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     uint64_t l2[2] = {0, 0};
     bool odd = false;        // a value that some rows do not attend is not finite
     bool ok = true;
-    for (int j = 0; j < steps[t]; ++j) {
+    for (int j = 0; j < my_steps; ++j) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[t], j & 1, a.err, SITE_PROMPT_SOFTMAX));
       if (!ok) break;
       tc_fence_after();
       uint32_t r[128];
+      const bool brief = my_short && j + 1 == my_steps;     // only the first half of the keys (so masked below)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, r + 32 * c);
+      for (int c = 0; c < 4; ++c)
+        if (c < 2 || !brief) tmem_ld32(s_col + 32 * c, r + 32 * c);
       tmem_wait_ld();
       tmem_regs_ready(r);
       const bool masked = j * 128 + 127 > pos_first;        // the same for the tile
@@ -448,19 +471,21 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+        if (h == 0 || !brief) {
+          uint32_t p[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const uint64_t x2 =
-              fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2);
-          float x, y;
-          unpair(x2, x, y);
-          x = fast_exp2(x);
-          y = fast_exp2(y);
-          l2[c & 1] = add2(l2[c & 1], pair(x, y));
-          p[c] = pack_bf16(x, y);
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t x2 =
+                fma2(pair(__uint_as_float(r[64 * h + 2 * c]), __uint_as_float(r[64 * h + 2 * c + 1])), sc2, ms2);
+            float x, y;
+            unpair(x2, x, y);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            l2[c & 1] = add2(l2[c & 1], pair(x, y));
+            p[c] = pack_bf16(x, y);
+          }
+          tmem_st32(s_col + 32 * h, p);
         }
-        tmem_st32(s_col + 32 * h, p);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -484,7 +509,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     const int head = kvh * a.G + row % a.G;
     const int64_t q_row = u.q_row + t * a.qt + row / a.G;
     __nv_bfloat16* out = a.O + q_row * a.o_stride + static_cast<int64_t>(head) * D;
-    if (ok && steps[t] > 0)
+    if (ok && my_steps > 0)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], 0, a.err, SITE_PROMPT_SOFTMAX));
     if (ok) {
       if (valid && a.lse) a.lse[q_row * a.h_q + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
@@ -503,7 +528,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          if (steps[t] > 0) {   // the same for the tile
+          if (my_steps > 0) {   // the same for the tile
             tmem_ld32(o_col + 32 * c, o);
             tmem_wait_ld();
             tmem_regs_ready(o);
@@ -528,22 +553,23 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::ISSUER) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::COLS);
   }
 }
 
-template <int D>
-cudaError_t run_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PromptArgs& a,
+template <int D, int TILES>
+cudaError_t run_prompt(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, PromptArgs a,
                        const LaunchCtx& c) {
-  using C = PromptShape<D>;
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  using C = PromptShape<D, TILES>;
+  a.n_units = a.n_q / (TILES * a.qt) + a.n_seq;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = static_cast<int64_t>(a.n_units) * a.h_kv;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  prompt_kernel<D><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, c.stream>>>(tmQ, tmK, tmV, a);
+  prompt_kernel<D, TILES><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, c.stream>>>(tmQ, tmK, tmV, a);
   note_launch();
   return cudaGetLastError();
 }
@@ -564,7 +590,6 @@ cudaError_t launch_prompt_attn(const ssa_prompt_params& p, const void* Q, const 
   a.n_seq = p.n_seq; a.n_q = p.n_q; a.n_kv = p.n_kv; a.h_q = p.h_q; a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;
   a.qt = 128 / a.G;
-  a.n_units = p.n_q / (2 * a.qt) + p.n_seq;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.err = c.err;
   // without key rows no unit loads any: the maps then describe the queries
@@ -576,7 +601,17 @@ cudaError_t launch_prompt_attn(const ssa_prompt_params& p, const void* Q, const 
       !encode_heads(&tmV, kv ? V : Q, p.d, kv ? p.h_kv : p.h_q, kv ? p.n_kv : p.n_q, kv ? p.v_stride : p.q_stride, 1,
                     128))
     return cudaErrorInvalidValue;
-  return p.d == 128 ? run_prompt<128>(tmQ, tmK, tmV, a, c) : run_prompt<64>(tmQ, tmK, tmV, a, c);
+  // One tile per block where a second would mostly be empty (64 prompts of one
+  // token, 32 heads on 8: 24 us with two tiles, 15 with one), where blocks of
+  // two would leave SMs idle (a prompt of 2000, eight kv-heads, d = 64: 34 us
+  // with two, 26 with one), and where they would need a second round that is
+  // not long (23 prompts of 48 tokens, eight kv-heads: 10.7 and 7.6 us; but a
+  // prompt of 8000, eight heads on one: 113 and 120 us).
+  const int64_t two = (static_cast<int64_t>(p.n_q) / (2 * a.qt) + p.n_seq) * p.h_kv;
+  if (p.n_q <= static_cast<int64_t>(a.qt) * p.n_seq || two < c.sm_count ||
+      (two < 2 * c.sm_count && p.n_kv <= static_cast<int64_t>(4096) * p.n_seq))
+    return p.d == 128 ? run_prompt<128, 1>(tmQ, tmK, tmV, a, c) : run_prompt<64, 1>(tmQ, tmK, tmV, a, c);
+  return p.d == 128 ? run_prompt<128, 2>(tmQ, tmK, tmV, a, c) : run_prompt<64, 2>(tmQ, tmK, tmV, a, c);
 }
 
 }  // namespace ssa

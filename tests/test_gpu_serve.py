@@ -662,6 +662,21 @@ def test_prompt(d, h_kv, G, lens):
     check_prompt(o, lse, q, k, v, qs, ks)
 
 
+@pytest.mark.parametrize("d,h_kv,G", [(128, 70, 4), (64, 60, 7), (128, 160, 1), (64, 40, 16)])
+@pytest.mark.parametrize("lens,kv_lens", [([1, 0, 200, 7], [1, 0, 200, 7]), ([130, 3], [260, 0])])
+def test_prompt_of_many_heads(d, h_kv, G, lens, kv_lens):
+    """Enough blocks for two tensor-core tiles each."""
+    r = rng_of("heads", d, h_kv, lens)
+    if len(lens) * h_kv < 2 * 148:
+        lens, kv_lens = lens * 6, kv_lens * 6
+    q, k, v, qs, ks = prompt_case(r, lens, kv_lens, h_kv, G, d)
+    v[int(ks[-1]):] = math.nan
+    o, lse = run_prompt(q, k, v, qs, ks)
+    pick = [0, h_kv // 2, h_kv - 1]                            # the oracle on three kv-heads
+    hd = [g * G + i for g in pick for i in range(G)]
+    check_prompt(o[:, hd], lse[:, hd], q[:, hd], k[:, pick], v[:, pick], qs, ks)
+
+
 @pytest.mark.parametrize("d,h_kv,G", [(128, 1, 4), (64, 2, 2)])
 @pytest.mark.parametrize("lens,kv_lens", [([1, 1, 1], [1, 128, 400]), ([40, 7], [300, 129]),       # keys before the prompt
                                           ([50, 9, 300], [20, 0, 130]), ([3], [0]), ([200], [1])])  # rows without keys
@@ -738,7 +753,9 @@ def test_prompt_offsets_that_do_not_fit():
     assert torch.equal(o, run_prompt(q, k, v, qs, ks)[0])
 
 
-@pytest.mark.parametrize("lens,h_kv,G,d", [([3000], 1, 8, 128), ([700, 1500, 33], 4, 4, 128), ([2049], 2, 2, 64)])
+@pytest.mark.parametrize("lens,h_kv,G,d", [([3000], 1, 8, 128), ([700, 1500, 33], 4, 4, 128), ([2049], 2, 2, 64),
+                                            ([3000, 1000], 8, 4, 128), ([2600], 4, 16, 64),
+                                            ([1500], 60, 1, 64)])
 def test_prompt_long(lens, h_kv, G, d):
     """Many steps and more units than SMs, against float64 on sampled rows."""
     r = rng_of("plong", lens)

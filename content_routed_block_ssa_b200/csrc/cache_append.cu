@@ -8,12 +8,18 @@
 // floor(tokens / page) + 2 pages, so the ranges never meet, and a warp finds
 // its sequence by a 32-way search without a pass over the lengths.
 //
-// Two kernels, by the tokens per sequence (see run_append): a block per
-// (unit, K or V, run of kv-heads) that keeps the page's tokens in registers
-// between the maximum and the rounding (each element is read once), and, for
-// decode steps, a warp per (unit, kv-head, K or V).  Bytes bound the first,
-// launch and the chain of dependent index loads the second.
+// A block takes one unit's K or V for a run of kv-heads.  With many tokens
+// all its threads share a head's rows; with few (decode steps, drafts) each
+// warp takes a head of its own, so that nothing waits at a barrier: a unit
+// decides for itself, whatever the others hold.  (Chosen by the average, a long
+// sequence among short ones was left to single warps: 43 us for 1024 tokens of
+// 512 sequences, one of them with half of the tokens, now 28.)  At most one
+// token per sequence on average takes a kernel of warps alone, in half the
+// registers (512 sequences: 16 us in blocks, 11 so).  Bytes bound long prompts,
+// launch and the chain of dependent index loads the rest.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -52,16 +58,26 @@ __device__ __forceinline__ AppendUnit append_unit(const AppendCfg& a, int64_t un
   AppendUnit u;
   u.n = 0;
   const auto start = [&](int s) { return min(max(__ldg(a.g.new_start + s), 0), a.n_tokens); };
-  int lo = 0, hi = a.n_seq;   // the sequence is in [lo, hi)
-  while (hi - lo > 1) {
+  // the sequence is in [lo, hi): cut by 32 to at most 128, then all at once
+  const auto before = [&](int s) { return start(s) / P + 2 * static_cast<int64_t>(s) <= unit; };
+  int lo = 0, hi = a.n_seq;
+  while (hi - lo > 128) {
     const int step = (hi - lo + 31) / 32;
     const int s = lo + lane * step;
-    const bool le = s < hi && start(s) / P + 2 * static_cast<int64_t>(s) <= unit;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, s < hi && before(s)));
     if (n == 0) return u;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
   }
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = lo + 32 * k + lane;
+    n += s < hi && before(s) ? 1 : 0;
+  }
+  n = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(n)));
+  if (n == 0) return u;
+  lo += n - 1;
   const int a0 = start(lo), a1 = max(start(lo + 1), a0);
   const int64_t j = unit - (a0 / P + 2 * static_cast<int64_t>(lo));
   const int have = __ldg(a.g.cached + lo);
@@ -172,15 +188,51 @@ __device__ __forceinline__ void copy_row8(Run4<T>* a, Run4<T>* b, const T* row, 
   }
 }
 
-// Prompts: a block per (unit, K or V, run of kv-heads).  The unit is looked up
-// and the angles are computed once for all the heads of the run; a head's rows
-// stay in registers between the maximum and the rounding, and the next heads'
-// are on their way to shared memory, each thread's to its own place (no
-// barrier but the one of the maximum).  64K tokens of eight heads: a block per
+// One head of a unit of few tokens, by a warp: the rows stay in registers
+// between the maximum and the rounding.
+template <typename T, int D, int P>
+__device__ __forceinline__ void append_head(const AppendCfg& a, const AppendUnit& u, bool is_k, int head, int page,
+                                            const LaneDims& at, const float (&w)[8], const uint64_t (&phase)[4]) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, F = kKeep;
+  const int lane = threadIdx.x & 31, row = lane / LPR;
+  const int64_t stride = is_k ? a.k_stride : a.v_stride;
+  const T* src = static_cast<const T*>(is_k ? a.g.K : a.g.V) + u.t0 * stride + static_cast<int64_t>(head) * D;
+  Row8<T> r[F];
+#pragma unroll
+  for (int k = 0; k < F; ++k)   // rows past the last repeat it: the same maximum
+    if (k * RPW < u.n) r[k].load(src + min(k * RPW + row, u.n - 1) * stride, at);
+  const int64_t ph = static_cast<int64_t>(page) * a.h_kv + head;
+  uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
+  float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
+  const float old = u.slot0 > 0 ? *scale : 0.f;
+  float x[F][8], f[F], amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < F; ++k) {
+    if (k * RPW >= u.n) continue;   // the same for the warp
+    Angles g;
+    if (is_k) g.set<sizeof(T) == 4>(at, phase, u.pos0 + min(k * RPW + row, u.n - 1), a.mscale);
+    f[k] = append_row<T, LPR>(a, is_k, r[k], at, w, g, x[k]);
+    amax = finite_amax(x[k], f[k], amax);
+  }
+  amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
+  const int e = page_exponent<D>(u, amax, old, codes, lane, 32);
+  const float inv = pow2(-e);
+#pragma unroll
+  for (int k = 0; k < F; ++k)
+    if (k * RPW + row < u.n) store_codes(codes + (u.slot0 + k * RPW + row) * D, at, x[k], f[k] * inv);
+  __syncwarp();   // every lane has read the old scale
+  if (lane == 0) *scale = pow2(e);
+}
+
+// A block per (unit, K or V, run of kv-heads).  With many tokens: the unit is
+// looked up and the angles are computed once for all the heads of the run; a
+// head's rows stay in registers between the maximum and the rounding, and the
+// next heads' are on their way to shared memory, each thread's to its own place
+// (no barrier but the one of the maximum).  64K tokens of eight heads: a block per
 // kv-head took 205 us, most of it the chain of index loads; the next head
 // alone on its way 115 us, bound by the bytes in flight.
 template <typename T, int D, int P>
-__global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1 : 2) append_page_kernel(const AppendCfg a) {
+__global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1 : 2) append_kernel(const AppendCfg a) {
   constexpr int LPR = D / 8, KEEP = kKeep, THREADS = P * LPR / KEEP, ROWS = THREADS / LPR;
   constexpr int STAGES = page_stages<T>();
   __shared__ float red[2][THREADS / 32];
@@ -194,6 +246,16 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1
   if (u.n == 0) return;
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
   const LaneDims at(sub, is_k ? a.rot : 0, a.layout);
+  if (u.n <= KEEP * (32 / LPR)) {   // the same for the block
+    const int page = unit_page(a, u, count);
+    if (page < 0) return;
+    float w[8];
+    uint64_t phase[4];
+    lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
+    at.phases(a.g.freq, sub, phase);
+    for (int h = h0 + warp; h < h1; h += THREADS / 32) append_head<T, D, P>(a, u, is_k, h, page, at, w, phase);
+    return;
+  }
   const T* src[KEEP];
 #pragma unroll
   for (int k = 0; k < KEEP; ++k)   // rows past the last repeat it: the same maximum
@@ -236,12 +298,17 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1
     const Run4<T>* from = ring + (h % STAGES) * (KEEP * 2 * THREADS);
     float x[KEEP][8], f[KEEP];
     float amax = 0.f;
+    const auto values = [&](auto all) {   // all: every thread has KEEP rows, nothing to test
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k) {
-      const Row8<T> r{from[2 * k * THREADS], from[(2 * k + 1) * THREADS]};
-      f[k] = append_row<T, LPR>(a, is_k, r, at, w, angles[k], x[k]);
-      amax = finite_amax(x[k], f[k], amax);
-    }
+      for (int k = 0; k < KEEP; ++k) {
+        if (!all && k * ROWS >= u.n) continue;   // the same for the block
+        const Row8<T> r{from[2 * k * THREADS], from[(2 * k + 1) * THREADS]};
+        f[k] = append_row<T, LPR>(a, is_k, r, at, w, angles[k], x[k]);
+        amax = finite_amax(x[k], f[k], amax);
+      }
+    };
+    if (u.n > (KEEP - 1) * ROWS) values(std::true_type{});
+    else values(std::false_type{});
     amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
     if (lane == 0) red[h & 1][warp] = amax;
     __syncthreads();   // the maxima are there, and every thread has the old scale
@@ -257,8 +324,8 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1
   }
 }
 
-// Decode steps: a warp per (unit, kv-head, K or V).  More rows than one pass
-// holds are read twice.
+// Decode steps, a token per sequence: a warp per (unit, kv-head, K or V), in half
+// the registers.  More rows than one pass holds are read twice.
 template <typename T, int D, int P>
 __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
@@ -314,24 +381,24 @@ cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
   const int64_t units = a.n_tokens / P + 2 * static_cast<int64_t>(a.n_seq);
   if (units > INT32_MAX || units * a.h_kv > INT32_MAX) return cudaErrorInvalidValue;
   a.n_units = static_cast<int32_t>(units);
-  if (a.n_tokens <= 16 * static_cast<int64_t>(a.n_seq)) {
-    const int64_t grid = (units * 2 * a.h_kv + 7) / 8;
-    append_few_kernel<T, D, P><<<static_cast<unsigned>(grid), 256, 0, c.stream>>>(a);
-  } else {
-    // all kv-heads in one run where the units alone give every SM work for
-    // four rounds of two blocks, else as many runs as that takes
-    int64_t runs = (8 * static_cast<int64_t>(c.sm_count) + 2 * units - 1) / (2 * units);
-    if (runs > a.h_kv) runs = a.h_kv;
-    a.per_run = static_cast<int32_t>((a.h_kv + runs - 1) / runs);
-    a.runs = (a.h_kv + a.per_run - 1) / a.per_run;
-    const int64_t grid = units * a.runs * 2;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    constexpr int kThreads = P * D / 8 / kKeep, kSmem = page_stages<T>() * kKeep * kThreads * 8 * sizeof(T);
-    const cudaError_t e =
-        cudaFuncSetAttribute(append_page_kernel<T, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    append_page_kernel<T, D, P><<<static_cast<unsigned>(grid), kThreads, kSmem, c.stream>>>(a);
+  if (a.n_tokens <= a.n_seq) {
+    append_few_kernel<T, D, P><<<static_cast<unsigned>((units * 2 * a.h_kv + 7) / 8), 256, 0, c.stream>>>(a);
+    note_launch();
+    return cudaGetLastError();
   }
+  // All kv-heads in one run where the units alone give every SM two blocks,
+  // else as many runs as that takes (more rounds of shorter blocks: 64
+  // sequences of five drafts 11.4 us at four rounds, 10.7 at one).
+  constexpr int kThreads = P * D / 8 / kKeep, kSmem = page_stages<T>() * kKeep * kThreads * 8 * sizeof(T);
+  int64_t runs = (2 * static_cast<int64_t>(c.sm_count) + 2 * units - 1) / (2 * units);
+  if (runs > a.h_kv) runs = a.h_kv;
+  a.per_run = static_cast<int32_t>((a.h_kv + runs - 1) / runs);
+  a.runs = (a.h_kv + a.per_run - 1) / a.per_run;
+  const int64_t grid = units * a.runs * 2;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(append_kernel<T, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  append_kernel<T, D, P><<<static_cast<unsigned>(grid), kThreads, kSmem, c.stream>>>(a);
   note_launch();
   return cudaGetLastError();
 }

@@ -4,11 +4,13 @@
 // A unit is up to 16 query rows that share a kv-head (new tokens x the G query
 // heads of the group; with selected blocks one token's G heads), and a unit's
 // keys are cut into `splits` runs, one block each, whose partial results a
-// second kernel joins.  Each of a block's three warps walks its own 32-key
-// pieces (every third of the run) with a ring of bulk copies of its own, so
-// no warp waits for another until the end.  The products are small against
-// the bytes (2 G flops per byte): the kernel is bound by reading codes, and
-// the instructions per code decide whether it keeps up:
+// second kernel joins.  Each of a block's three warps walks its own pieces of
+// 4 KB of keys and of values (every third of the run) with a ring of bulk
+// copies of its own, so no warp waits for another until the end.  The products
+// are small against the bytes (2 G flops per byte): the kernel is bound by
+// reading codes (64 sequences of up to 16K tokens, 32 heads on 8, d = 128: 224
+// to 243 us by the box, 85 to 91% of the copy rate), and the instructions per
+// code decide whether it keeps up:
 //
 //  * the keys and the value dims are the M = 16 rows of the m16n8k16 products
 //    (S^T = K Q^T, O^T = V^T P^T) and the query rows their N = 8 columns: a
@@ -38,9 +40,10 @@
 namespace ssa {
 namespace {
 
-constexpr int kPiece = 32;     // keys per piece
+// Keys per piece: 4 KB of keys (a piece has a fixed cost of some 150 instructions).
+constexpr int piece_keys(int d) { return d == 64 ? 64 : 32; }
 constexpr int kWarps = 3;
-constexpr int kBlocks = 4;     // blocks per SM (3 with 16 rows a unit, by registers)
+constexpr int kBlocks = 4;     // blocks per SM
 constexpr int kMaxEnt = 32 + 4032 / 64 + 2;   // selected blocks and window blocks
 constexpr int kSmCount = 148;
 
@@ -59,7 +62,8 @@ struct CacheCfg {
 
 template <int D>
 struct CacheShape {
-  static constexpr int K_BYTES = kPiece * D;
+  static constexpr int PIECE = piece_keys(D);
+  static constexpr int K_BYTES = PIECE * D;
   static constexpr int STAGE = 2 * K_BYTES;
   static constexpr int STAGES = 16384 / STAGE;
   static constexpr int RING = STAGES * STAGE;
@@ -67,7 +71,7 @@ struct CacheShape {
   static constexpr int BARS = kWarps * RING;
   static constexpr int ENTS = BARS + kWarps * STAGES * 8;
   static constexpr int SMEM = ENTS + (kMaxEnt + 1) * 8;
-  static_assert(kWarps * 16 * (OROW + 2) * 4 <= kWarps * RING, "the join fits the rings");
+  static_assert(kWarps * 16 * (OROW + 2) * 4 <= BARS, "the join fits the rings");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -134,6 +138,7 @@ template <int D, bool SEL, int R>
 __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_kernel(const CacheCfg a) {
   using C = CacheShape<D>;
   constexpr int MT = D / 16;    // output tiles of 16 dims
+  constexpr int QT = C::PIECE / 16;   // key tiles of a piece
   constexpr int VW = D / 32;    // words of a value row per lane
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
       const int r = 8 * n + 2 * t + c;
       pos[n][c] = r < n_rows ? first + (r0 + r) / a.G : -1;
     }
-  const int ppb = a.page / kPiece;
+  const int ppb = a.page / C::PIECE;
   const int wlo = SEL ? max(pos_hi - a.window + 1, 0) : 0;
 
   if (lane == 0)
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
     n_pieces = ents[kMaxEnt].x * ppb;
   } else {
     __syncwarp();
-    n_pieces = pos_hi >= 0 ? pos_hi / kPiece + 1 : 0;
+    n_pieces = pos_hi >= 0 ? pos_hi / C::PIECE + 1 : 0;
   }
   const int c0 = static_cast<int>(static_cast<int64_t>(n_pieces) * split / a.splits);
   const int c1 = static_cast<int>(static_cast<int64_t>(n_pieces) * (split + 1) / a.splits);
@@ -237,13 +242,13 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
       } else {
         page = __ldg(table + blk);
       }
-      p.key0 = blk * a.page + (c % ppb) * kPiece;
+      p.key0 = blk * a.page + (c % ppb) * C::PIECE;
       if (page >= 0 && page < a.n_pages) {
         p.page = page;
         const int64_t ph = static_cast<int64_t>(page) * a.h_kv + kvh;
         p.ks = __ldg(a.g.ks + ph);
         p.vs = __ldg(a.g.vs + ph);
-      } else if (a.g.bad) {
+      } else if (a.g.bad && p.key0 % a.page == 0) {
         atomicAdd(a.g.bad, 1);
       }
     }
@@ -317,11 +322,11 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
       const uint8_t* sK = ring + st * C::STAGE;
       const uint8_t* sV = sK + C::K_BYTES;
       const float lvs = log2f(vs), ivs = 1.f / vs;
-      const bool partial = key0 + kPiece - 1 > pos_lo || key0 < lo;
+      const bool partial = key0 + C::PIECE - 1 > pos_lo || key0 < lo;
       // S^T = K Q^T: keys 16 q + g (c = 0, 1) and + 8 (c = 2, 3) of this lane
-      float S[R][2][4];
+      float S[R][QT][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < QT; ++q) {
 #pragma unroll
         for (int n = 0; n < R; ++n)
 #pragma unroll
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
         for (int c = 0; c < 2; ++c) {
           const float f = qf[n][c] * ks;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < QT; ++q) {
             S[n][q][c] = fmaf(S[n][q][c], f, lvs);
             S[n][q][2 + c] = fmaf(S[n][q][2 + c], f, lvs);
             if (partial) {
@@ -357,7 +362,9 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
               if (kp + 8 > pos[n][c] || kp + 8 < lo) S[n][q][2 + c] = -INFINITY;
             }
           }
-          m[n][c] = fmaxf(fmaxf(S[n][0][c], S[n][0][2 + c]), fmaxf(S[n][1][c], S[n][1][2 + c]));
+          m[n][c] = fmaxf(S[n][0][c], S[n][0][2 + c]);
+#pragma unroll
+          for (int q = 1; q < QT; ++q) m[n][c] = fmaxf(m[n][c], fmaxf(S[n][q][c], S[n][q][2 + c]));
         }
       }
 #pragma unroll
@@ -386,13 +393,13 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
             for (int c = 0; c < 4; ++c) O[n][j][c] *= x[c & 1];
         }
       }
-      uint32_t P[R][2][2];
+      uint32_t P[R][QT][2];
 #pragma unroll
       for (int n = 0; n < R; ++n) {
         const float ra = M[n][0] == -INFINITY ? 0.f : M[n][0], rb = M[n][1] == -INFINITY ? 0.f : M[n][1];
         float sa = 0.f, sb = 0.f;
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < QT; ++q)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float x = fast_exp2(S[n][q][2 * k] - ra), y = fast_exp2(S[n][q][2 * k + 1] - rb);
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
       // O^T += V^T P^T: keys 16 q + {2t, 2t+1, 2t+8, 2t+9}
       uint32_t odd = 0;   // NaN among values that not every row attends
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < QT; ++q) {
         uint32_t v[4][VW];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
         // 0 * NaN is NaN: such values stay out of the product and reach the
         // rows that attend them here
         const float bad = __int_as_float(0x7FFFFFFF);
-        for (int key = 0; key < kPiece; ++key) {
+        for (int key = 0; key < C::PIECE; ++key) {
           const int kp = key0 + key;
           if (kp > pos_hi || kp < lo) continue;
 #pragma unroll
@@ -613,31 +620,40 @@ Split split_of(const ssa_cache_attn_params& p) {
   Split s;
   const int G = p.h_q / p.h_kv;
   const bool sel = p.topk > 0;
-  s.unit_rows = (sel ? G : p.n_q * G) <= 8 ? 8 : 16;
-  s.tiles = sel ? p.n_q : (p.n_q * G + s.unit_rows - 1) / s.unit_rows;
-  s.rows = sel ? G : (p.n_q * G < s.unit_rows ? p.n_q * G : s.unit_rows);
+  // A unit of 24 rows was tried for 17 to 24 (five drafts of four heads): 105 us
+  // in place of 114 at d = 128, 133 in place of 128 at d = 64, at 255 registers.
+  const int rows = sel ? G : p.n_q * G;
+  s.unit_rows = rows <= 8 ? 8 : 16;
+  s.tiles = sel ? p.n_q : (rows + s.unit_rows - 1) / s.unit_rows;
+  s.rows = rows < s.unit_rows ? rows : s.unit_rows;
   s.units = static_cast<int64_t>(p.n_seq) * p.h_kv * s.tiles;
-  int64_t pieces = static_cast<int64_t>(p.max_pages) * p.page / kPiece;
+  int64_t pieces = static_cast<int64_t>(p.max_pages) * p.page / piece_keys(p.d);
   if (sel) {
-    const int64_t most = (p.topk + p.window / p.page + 2) * static_cast<int64_t>(p.page / kPiece);
+    const int64_t most = (p.topk + p.window / p.page + 2) * static_cast<int64_t>(p.page / piece_keys(p.d));
     if (pieces > most) pieces = most;
   }
-  // kBlocks blocks per SM run at a time: one wave of them when the units are
-  // few, else about four, so that ragged lengths even out; at least four
-  // pieces per warp
+  // One wave of the blocks that run at a time when the units are few, down to
+  // one piece per warp (a latency: a sequence of 1000 took 14 us at four pieces
+  // per warp, 10 at one); else about four waves, so that ragged lengths even
+  // out, with at least four pieces per warp.
   const int64_t room = kBlocks * kSmCount;
-  int64_t n = s.units < 1 ? 1 : s.units * 8 < room ? room / s.units : (4 * room + s.units - 1) / s.units;
-  if (sel && s.units * 8 >= room) {
-    // units of one size: the split that costs least, a block's set-up and join
-    // counted as six pieces of a warp
-    int64_t best = 0, cost = INT64_MAX;
-    for (int64_t k = 1; k <= 8; ++k) {
-      const int64_t c = (s.units * k + room - 1) / room * (pieces + 6 * kWarps * k) * 840 / k;
-      if (c < cost) { cost = c; best = k; }
+  int64_t n = 1;
+  if (s.units * 8 < room) {
+    n = room / (s.units < 1 ? 1 : s.units);
+    if (n > pieces / kWarps) n = pieces / kWarps;
+  } else {
+    n = (4 * room + s.units - 1) / s.units;
+    if (sel) {
+      // units of one size: the split that costs least, a block's set-up and
+      // join counted as six pieces of a warp
+      int64_t cost = INT64_MAX;
+      for (int64_t k = 1; k <= 8; ++k) {
+        const int64_t c = (s.units * k + room - 1) / room * (pieces + 6 * kWarps * k) * 840 / k;
+        if (c < cost) { cost = c; n = k; }
+      }
     }
-    n = best;
+    if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
   }
-  if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
   s.splits = static_cast<int>(n < 1 ? 1 : n);
   return s;
 }

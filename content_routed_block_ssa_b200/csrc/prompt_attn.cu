@@ -75,16 +75,26 @@ __device__ __forceinline__ PromptUnit prompt_unit(const PromptArgs& a, int rows,
   const int lane = threadIdx.x & 31;
   PromptUnit u{};
   const auto start = [&](int s) { return min(max(__ldg(a.q_start + s), 0), a.n_q); };
+  // the sequence is in [lo, hi): cut by 32 to at most 128, then all at once
+  const auto before = [&](int s) { return start(s) / rows + s <= unit; };
   int lo = 0, hi = a.n_seq;
-  while (hi - lo > 1) {
+  while (hi - lo > 128) {
     const int step = (hi - lo + 31) / 32;
     const int s = lo + lane * step;
-    const bool le = s < hi && start(s) / rows + s <= unit;
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, s < hi && before(s)));
     if (n == 0) return u;
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
   }
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int s = lo + 32 * k + lane;
+    n += s < hi && before(s) ? 1 : 0;
+  }
+  n = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(n)));
+  if (n == 0) return u;
+  lo += n - 1;
   const int a0 = start(lo), a1 = max(start(lo + 1), a0);
   const int64_t q0 = static_cast<int64_t>(unit - (a0 / rows + lo)) * rows;
   if (q0 < 0 || q0 >= a1 - a0) return u;

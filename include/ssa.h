@@ -593,9 +593,10 @@ SSA_API size_t ssa_cache_attn_workspace_size(const ssa_cache_attn_params* p);
  *   O          device output [n_seq, n_q, h_q, d] bf16
  *   lse        device float32 output [n_seq, n_q, h_q], may be NULL: natural
  *              log of the sum of exp(scale q.k)
- *   bad_count  device int32, may be NULL: counts block_idx entries and 32-key
- *              pieces of pages skipped (a piece once for each row group that
- *              would read it)
+ *   bad_count  device int32, may be NULL: counts block_idx entries and pages
+ *              skipped (a page once for each group of rows that would read it:
+ *              up to 16 rows of new tokens x query heads of a kv-head, with
+ *              blocks one token's)
  *   ws         device workspace of ssa_cache_attn_workspace_size(p) bytes;
  *              calls that may overlap need one each
  */

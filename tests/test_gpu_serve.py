@@ -581,7 +581,7 @@ def test_cache_attention_pages_outside_the_pool_are_left_out():
     bad = torch.zeros(1, dtype=torch.int32, device="cuda")
     o, lse, _ = run_cache(q, lens, table, codes, scale, page, bad=bad)
     check_cache(o, lse, q, lens, table, codes, scale, page)
-    assert int(bad) == 3 * 2 * 2                              # pieces of 32 keys, for each of two kv-heads
+    assert int(bad) == 3 * 2                                  # pages, for each of two kv-heads
     table[:] = -1                                             # nothing left: every row is empty
     o, lse, _ = run_cache(q, lens, table, codes, scale, page)
     assert not o.any() and (lse == -math.inf).all()

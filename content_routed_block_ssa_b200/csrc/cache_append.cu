@@ -122,11 +122,10 @@ __device__ __forceinline__ float finite_amax(const float (&x)[8], float f, float
   return fmaxf(m, r);
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* row, const LaneDims& at, const float (&x)[8], float inv) {
-  *reinterpret_cast<uint32_t*>(row + at.a) =
-      to_e4m3x2(x[0] * inv, x[1] * inv) | to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
-  *reinterpret_cast<uint32_t*>(row + at.b) =
-      to_e4m3x2(x[4] * inv, x[5] * inv) | to_e4m3x2(x[6] * inv, x[7] * inv) << 16;
+__device__ __forceinline__ void store_codes(uint8_t* row, const LaneDims& at, float (&x)[8], float inv) {
+  scale_row(x, inv);
+  *reinterpret_cast<uint32_t*>(row + at.a) = to_e4m3x2(x[0], x[1]) | to_e4m3x2(x[2], x[3]) << 16;
+  *reinterpret_cast<uint32_t*>(row + at.b) = to_e4m3x2(x[4], x[5]) | to_e4m3x2(x[6], x[7]) << 16;
 }
 
 // Rounds 16 codes again to a scale 2^-down times coarser.
@@ -157,8 +156,7 @@ __device__ __forceinline__ float append_row(const AppendCfg& a, bool is_k, const
   r.get(x);
   if (!is_k) return 1.f;
   const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= w[i];
+  scale_row(x, w);
   g.turn(at, x);
   return f;
 }

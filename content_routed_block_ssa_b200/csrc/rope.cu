@@ -162,20 +162,25 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) rope_stream_kernel(const
     ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], parity >> stage & 1u, a.err, SITE_ROPE_FULL));
     if (!ok) break;
     parity ^= 1u << stage;
-#pragma unroll 4
-    for (int h0 = 0; h0 < heads; h0 += RPW) {
-      const int h = h0 + hr;
-      T* row = rows + min(h, heads - 1) * D;
-      Row8<T> r;
-      r.load(row, at);
-      float x[8];
-      r.get(x);
-      const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
+    const auto turn_rows = [&](int n) {   // n known for whole pieces: nothing to test
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * w[i] * f;
-      angles.turn(at, x);
-      if (h < heads) Row8<T>::store(row, at, x);
-    }
+      for (int h0 = 0; h0 < CH; h0 += RPW) {
+        if (h0 >= n) break;
+        const int h = h0 + hr;
+        T* row = rows + min(h, n - 1) * D;
+        Row8<T> r;
+        r.load(row, at);
+        float x[8];
+        r.get(x);
+        const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
+        scale_row(x, w);
+        angles.turn(at, x);
+        scale_row(x, f);
+        if (h < n) Row8<T>::store(row, at, x);
+      }
+    };
+    if (heads == CH) turn_rows(CH);
+    else turn_rows(heads);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {

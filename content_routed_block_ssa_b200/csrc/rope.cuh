@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "common.cuh"
 #include "ssa.h"
 
 namespace ssa {
@@ -139,18 +140,20 @@ struct Angles {
       }
     }
   }
-  // Turns a row's dims in place; a dim that does not turn takes nothing from
-  // its neighbour, infinities neither.
+  // Turns a row's dims in place, two pairs at a time; a dim that does not turn
+  // takes nothing from its neighbour, infinities neither.
   __device__ __forceinline__ void turn(const LaneDims& at, float (&x)[8]) const {
+    const uint64_t minus = pair(-1.f, -1.f);
+    if (!at.rotated) return;
     if (at.half) {
-      if (at.rotated)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[i], b = x[i + 4];
-          x[i] = fmaf(-b, s[i], a * c[i]);
-          x[i + 4] = fmaf(a, s[i], b * c[i]);
-        }
-    } else if (at.rotated) {
+      for (int i = 0; i < 4; i += 2) {
+        const uint64_t a = pair(x[i], x[i + 1]), b = pair(x[i + 4], x[i + 5]);
+        const uint64_t co = pair(c[i], c[i + 1]), si = pair(s[i], s[i + 1]);
+        unpair(fma2(mul2(b, si), minus, mul2(a, co)), x[i], x[i + 1]);
+        unpair(fma2(a, si, mul2(b, co)), x[i + 4], x[i + 5]);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = x[2 * i], b = x[2 * i + 1];
@@ -160,6 +163,16 @@ struct Angles {
     }
   }
 };
+
+// x[i] *= w[i], x[i] *= f.
+__device__ __forceinline__ void scale_row(float (&x)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) unpair(mul2(pair(x[i], x[i + 1]), pair(w[i], w[i + 1])), x[i], x[i + 1]);
+}
+__device__ __forceinline__ void scale_row(float (&x)[8], float f) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) unpair(mul2(pair(x[i], x[i + 1]), pair(f, f)), x[i], x[i + 1]);
+}
 
 // A position's rotation with the weights of a head's dims folded in:
 // y[i] = x[i] * c[i] + x[partner of i] * s[i].
@@ -204,12 +217,11 @@ struct Turn {
 // 1 / sqrt(mean(x^2) + eps) over the LPR lanes of a row.
 template <int LPR>
 __device__ __forceinline__ float norm_factor(const float (&x)[8], float eps) {
-  float q = x[0] * x[0], p = x[1] * x[1];
+  uint64_t q2 = mul2(pair(x[0], x[1]), pair(x[0], x[1]));
 #pragma unroll
-  for (int i = 2; i < 8; i += 2) {
-    q = fmaf(x[i], x[i], q);
-    p = fmaf(x[i + 1], x[i + 1], p);
-  }
+  for (int i = 2; i < 8; i += 2) q2 = fma2(pair(x[i], x[i + 1]), pair(x[i], x[i + 1]), q2);
+  float q, p;
+  unpair(q2, q, p);
   q += p;
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);

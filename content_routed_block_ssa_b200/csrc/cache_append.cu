@@ -107,12 +107,16 @@ __device__ __forceinline__ int unit_page(const AppendCfg& a, const AppendUnit& u
   return -1;
 }
 
-// The largest finite |x| * f of a row's elements and m (fmaxf leaves NaN out).
-__device__ __forceinline__ float finite_amax(const float (&x)[8], float f, float m) {
+__device__ __forceinline__ float row_amax(const float (&x)[8]) {
   float r = fabsf(x[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) r = fmaxf(r, fabsf(x[i]));
-  r *= f;
+  return r;
+}
+
+// The largest finite |x| * f of a row's elements and m (fmaxf leaves NaN out).
+__device__ __forceinline__ float finite_amax(const float (&x)[8], float f, float m) {
+  float r = row_amax(x) * f;
   if (!(r < INFINITY)) {   // among them an infinity (or all NaN): one by one
     r = 0.f;
 #pragma unroll
@@ -289,36 +293,48 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1
   const int64_t ph = static_cast<int64_t>(page) * a.h_kv + h0;
   uint8_t* codes = (is_k ? a.g.kc : a.g.vc) + ph * (P * D);
   float* scale = (is_k ? a.g.ks : a.g.vs) + ph;
-  for (int h = h0; h < h1; ++h, codes += P * D, ++scale) {
-    const float old = u.slot0 > 0 ? *scale : 0.f;
-    fetch(h + STAGES - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-    const Run4<T>* from = ring + (h % STAGES) * (KEEP * 2 * THREADS);
-    float x[KEEP][8], f[KEEP];
-    float amax = 0.f;
-    const auto values = [&](auto all) {   // all: every thread has KEEP rows, nothing to test
+  // key: K, not V; whole: a full page, nothing to test
+  const auto heads = [&](auto key, auto whole) {
+    for (int h = h0; h < h1; ++h, codes += P * D, ++scale) {
+      const float old = !whole && u.slot0 > 0 ? *scale : 0.f;
+      fetch(h + STAGES - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      const Run4<T>* from = ring + (h % STAGES) * (KEEP * 2 * THREADS);
+      float x[KEEP][8], f[KEEP];
+      float amax = 0.f;
 #pragma unroll
       for (int k = 0; k < KEEP; ++k) {
-        if (!all && k * ROWS >= u.n) continue;   // the same for the block
+        if (!whole && k * ROWS >= u.n) continue;   // the same for the block
         const Row8<T> r{from[2 * k * THREADS], from[(2 * k + 1) * THREADS]};
-        f[k] = append_row<T, LPR>(a, is_k, r, at, w, angles[k], x[k]);
-        amax = finite_amax(x[k], f[k], amax);
+        f[k] = append_row<T, LPR>(a, key, r, at, w, angles[k], x[k]);
+        amax = fmaxf(amax, row_amax(x[k]) * f[k]);   // fmaxf leaves NaN out
       }
-    };
-    if (u.n > (KEEP - 1) * ROWS) values(std::true_type{});
-    else values(std::false_type{});
-    amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
-    if (lane == 0) red[h & 1][warp] = amax;
-    __syncthreads();   // the maxima are there, and every thread has the old scale
-    amax = __uint_as_float(
-        __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(red[h & 1][lane % (THREADS / 32)])));
-    const int e = page_exponent<D>(u, amax, old, codes, threadIdx.x, THREADS);
-    const float inv = pow2(-e);
-    uint8_t* to = codes + (u.slot0 + row) * D;
+      if (amax == INFINITY) {   // infinities are left out too: one by one
+        amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-      if (row + k * ROWS < u.n) store_codes(to + k * ROWS * D, at, x[k], f[k] * inv);
-    if (threadIdx.x == 0) *scale = pow2(e);
+        for (int k = 0; k < KEEP; ++k)
+          if (whole || k * ROWS < u.n) amax = finite_amax(x[k], f[k], amax);
+      }
+      amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // both orders agree from 0 up
+      if (lane == 0) red[h & 1][warp] = amax;
+      __syncthreads();   // the maxima are there, and every thread has the old scale
+      amax = __uint_as_float(
+          __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(red[h & 1][lane % (THREADS / 32)])));
+      const int e = page_exponent<D>(u, amax, old, codes, threadIdx.x, THREADS);
+      const float inv = pow2(-e);
+      uint8_t* to = codes + (u.slot0 + row) * D;
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k)
+        if (whole || row + k * ROWS < u.n) store_codes(to + k * ROWS * D, at, x[k], key ? f[k] * inv : inv);
+      if (threadIdx.x == 0) *scale = pow2(e);
+    }
+  };
+  if (u.n == P) {
+    if (is_k) heads(std::true_type{}, std::true_type{});
+    else heads(std::false_type{}, std::true_type{});
+  } else {
+    if (is_k) heads(std::true_type{}, std::false_type{});
+    else heads(std::false_type{}, std::false_type{});
   }
 }
 

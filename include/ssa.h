@@ -427,17 +427,18 @@ SSA_API ssa_status ssa_route_hier(const ssa_params* p, const ssa_hier_params* hp
  * and causal attention over packed prompts of different lengths.  The
  * conventions above hold (caller-owned device buffers, 16-byte aligned,
  * arguments checked before any launch, asynchronous on `stream`, launched on
- * the current device).  Tokens of an operand marked "strided" may lie further
- * apart than their heads take: token t, head h starts at element
- * t * stride + h * d, so that the heads of a joint q/k/v projection are used
- * where they are; a stride is at least heads * d elements and a multiple of
- * 16 bytes.
+ * the current device); outputs overlap no operand unless a call says so.
+ * Tokens of an operand marked "strided" may lie further apart than their
+ * heads take: token t, head h starts at element t * stride + h * d, so that
+ * the heads of a joint q/k/v projection are used where they are; a stride is
+ * at least heads * d elements and a multiple of 16 bytes.
  *
  * Lengths, offsets, page numbers and positions are read on the GPU.  Values
  * that do not fit (a page outside the pool, a length beyond the page table, a
  * decreasing offset) never address memory: the tokens or keys that they name
  * are left out and, where the call has a bad_count, counted into it
- * (atomically added, not reset).
+ * (atomically added, not reset).  Where offsets decrease, tokens of the
+ * other sequences may be left out with them, and none of these are counted.
  */
 
 /* Pairing of the rotated dims: (i, i + rot/2), or (2i, 2i + 1). */
@@ -511,8 +512,8 @@ SSA_API ssa_status ssa_qk_rope(const ssa_rope_params* p, const void* Q, const vo
  *   page_table        device int32 [n_seq, max_pages]: token j of sequence s
  *                     lies in slot j % page of page page_table[s][j / page];
  *                     entries behind a sequence's last page are not read
- * A page may stand in several sequences' rows (a shared prefix) as long as
- * no call appends to it through more than one of them.
+ * A page may stand in several places of the table (a shared prefix) as long
+ * as no call appends to it through more than one of them.
  */
 
 /* 72 bytes, no padding. */
@@ -586,6 +587,8 @@ SSA_API size_t ssa_cache_attn_workspace_size(const ssa_cache_attn_params* p);
  * them.  kv_len below 0 counts as 0; beyond max_pages * page it is cut to
  * that.  Logits, softmax and sums are float32; the probabilities enter
  * the second product as float16, relative to the row's running maximum.
+ * Meant for few new tokens (decode, drafts): with topk = 0 every 16 rows of
+ * tokens x query heads of a kv-head read the sequence's cache once.
  *   Q          device [n_seq, n_q, h_q, d] bf16
  *   kv_len     device int32 [n_seq]
  *   block_idx  device int32 [n_seq, n_q, h_kv, topk] (ssa_route_topk's

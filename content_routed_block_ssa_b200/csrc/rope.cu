@@ -11,7 +11,7 @@
 // loads ahead (128K tokens of 40 heads, d = 128, bf16: 449 to 457 us, 90% of the
 // copy rate; straight from registers 508 at best); with few, the heads of a
 // token are spread over several warps that load straight to registers, which
-// starts sooner (5003 tokens of 16 heads, d = 64, float32: 12.3 us, streamed 16.3).
+// starts sooner.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -30,40 +30,19 @@ struct RopeArgs {
   int64_t qs, ks, qos, kos;
   int32_t n_tokens, h_q, h_kv, rot, layout, norm;
   int32_t runs, per_run;   // runs of heads per token, head groups per run
+  int32_t even;            // pieces dealt out evenly to the warps, not tokens
   float eps, mscale;
   uint32_t* err;
 };
 
-// The heads g * RPW + hr, g in [g0, g1), of one of the two operands.
-template <typename T, int D>
-__device__ __forceinline__ void rope_heads(const T* in, T* out, int heads, int g0, int g1, const float* weight,
-                                           const LaneDims& at, const Angles& angles, const RopeArgs& a, int hr) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  constexpr int U = 2;   // head groups in flight
-  float w[8];
-  lane_weights(weight, at, w);
-  Turn turn;
-  turn.set(at, angles, w);
-  for (int g = g0; g < g1; g += U) {
-    Row8<T> r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u].load(in + static_cast<int64_t>(min((g + u) * RPW + hr, heads - 1)) * D, at);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (g + u >= g1) break;   // the same for the whole warp
-      const int h = (g + u) * RPW + hr;
-      float x[8], y[8];
-      r[u].get(x);
-      const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
-      turn.apply(at, x, f, y);
-      if (h < heads) Row8<T>::store(out + static_cast<int64_t>(h) * D, at, y);
-    }
-  }
-}
+constexpr int kGroups = 2;   // head groups in flight per warp
+constexpr int kDirect = 3;   // blocks per SM
 
+// An item is a run of a token's head groups (RPW heads each, those of the
+// queries first).  The first groups' loads start before the angles are computed.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;   // lanes per head, heads per warp
+__global__ void __launch_bounds__(256, kDirect) rope_kernel(const RopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = kGroups;   // lanes per head, heads per warp
   const int lane = threadIdx.x & 31, sub = lane % LPR, hr = lane / LPR;
   const int gq = (a.h_q + RPW - 1) / RPW, gk = (a.h_kv + RPW - 1) / RPW;
   const LaneDims at(sub, a.rot, a.layout);
@@ -74,18 +53,49 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_kernel(const
        item += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t token = item / a.runs;
     const int g0 = static_cast<int>(item % a.runs) * a.per_run, g1 = min(g0 + a.per_run, gq + gk);
+    const T* q = static_cast<const T*>(a.Q) + token * a.qs;
+    const T* k = static_cast<const T*>(a.K) + token * a.ks;
+    Row8<T> r[U];
+    const auto load = [&](int g) {   // U groups from g on, heads past the last repeat it
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = min(g + u, g1 - 1);
+        r[u].load(x < gq ? q + static_cast<int64_t>(min(x * RPW + hr, a.h_q - 1)) * D
+                         : k + static_cast<int64_t>(min((x - gq) * RPW + hr, a.h_kv - 1)) * D,
+                  at);
+      }
+    };
+    const int32_t pos = a.rot > 0 ? __ldg(a.pos + token) : 0;
+    load(g0);
     Angles angles;
-    angles.set<sizeof(T) == 4>(at, phase, a.rot > 0 ? __ldg(a.pos + token) : 0, a.mscale);
-    if (g0 < gq)
-      rope_heads<T, D>(static_cast<const T*>(a.Q) + token * a.qs, static_cast<T*>(a.Qo) + token * a.qos, a.h_q, g0,
-                       min(g1, gq), a.qw, at, angles, a, hr);
-    if (g1 > gq)
-      rope_heads<T, D>(static_cast<const T*>(a.K) + token * a.ks, static_cast<T*>(a.Ko) + token * a.kos, a.h_kv,
-                       max(g0 - gq, 0), g1 - gq, a.kw, at, angles, a, hr);
+    angles.set<sizeof(T) == 4>(at, phase, pos, a.mscale);
+    for (int g = g0; g < g1; g += U) {
+      if (g > g0) load(g);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (g + u >= g1) break;   // the same for the whole warp
+        const bool is_q = g + u < gq;
+        const int h = (is_q ? g + u : g + u - gq) * RPW + hr;
+        float x[8], w[8];
+        r[u].get(x);
+        const float f = a.norm ? norm_factor<LPR>(x, a.eps) : 1.f;
+        const float* weight = is_q ? a.qw : a.kw;
+        if (weight) {   // from the cache: registers go to the loads
+          lane_weights(weight, at, w);
+          scale_row(x, w);
+        }
+        angles.turn(at, x);
+        scale_row(x, f);
+        if (h < (is_q ? a.h_q : a.h_kv))
+          Row8<T>::store((is_q ? static_cast<T*>(a.Qo) + token * a.qos : static_cast<T*>(a.Ko) + token * a.kos) +
+                             static_cast<int64_t>(h) * D,
+                         at, x);
+      }
+    }
   }
 }
 
-constexpr int kStreamFrom = 4;   // pieces per warp
+constexpr int kEvenBelow = 4;    // tokens per warp
 constexpr int kStreamWarps = 24, kStages = 4, kStageBytes = 2048;
 constexpr int kStreamSmem = kStreamWarps * kStages * (kStageBytes + 8);
 
@@ -110,21 +120,26 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) rope_stream_kernel(const
   lane_weights(a.qw, at, qw);
   lane_weights(a.kw, at, kw);
 
-  // this warp's tokens, `cq` pieces of queries and `ck` of keys each
+  // A token has `cq` pieces of queries and `ck` of keys.  With several tokens
+  // per warp every tokens-th is this warp's, whole; with fewer (a.even) the
+  // pieces are dealt out evenly, in runs.
   const int cq = (a.h_q + CH - 1) / CH, ck = (a.h_kv + CH - 1) / CH, per = cq + ck;
   const int first = blockIdx.x * kStreamWarps + warp, every = gridDim.x * kStreamWarps;
-  struct Place {   // a piece: token first + k * every, piece c
+  const int step = a.even ? 1 : every;
+  struct Place {   // piece c of a token, and how many are left from it on
     int64_t token;
     int c;
-    __device__ __forceinline__ void next(int per, int every) {
-      if (++c == per) { c = 0; token += every; }
+    int32_t left;   // (a piece holds at least 128 bytes)
+    __device__ __forceinline__ void next(int per, int step) {
+      --left;
+      if (++c == per) { c = 0; token += step; }
     }
   };
   const auto heads_of = [&](const Place& w) {
     return w.c < cq ? min(CH, a.h_q - w.c * CH) : min(CH, a.h_kv - (w.c - cq) * CH);
   };
   const auto load = [&](const Place& w, int stage) {
-    if (w.token >= a.n_tokens) return;
+    if (w.left <= 0) return;
     if (lane == 0) {
       const T* src = w.c < cq ? static_cast<const T*>(a.Q) + w.token * a.qs + static_cast<int64_t>(w.c) * (CH * D)
                               : static_cast<const T*>(a.K) + w.token * a.ks + static_cast<int64_t>(w.c - cq) * (CH * D);
@@ -133,26 +148,33 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) rope_stream_kernel(const
       bulk_load(ring + stage * kStageBytes, src, bytes, &full[stage]);
     }
   };
-  Place now{first, 0}, ahead{first, 0};
+  Place now{first, 0, first < a.n_tokens ? ((a.n_tokens - 1 - first) / every + 1) * per : 0};
+  if (a.even) {
+    const int64_t all = static_cast<int64_t>(a.n_tokens) * per, p0 = all * first / every;
+    now = Place{p0 / per, static_cast<int>(p0 % per), static_cast<int32_t>(all * (first + 1) / every - p0)};
+  }
+  Place ahead = now;
   load(ahead, 0);
-  ahead.next(per, every);
+  ahead.next(per, step);
   load(ahead, 1);
-  ahead.next(per, every);
-  int32_t pos = a.rot > 0 && now.token < a.n_tokens ? __ldg(a.pos + now.token) : 0;
+  ahead.next(per, step);
+  int32_t pos = a.rot > 0 && now.left > 0 ? __ldg(a.pos + now.token) : 0;
   Angles angles;
+  bool turned = false;   // `angles` are the token's
   uint32_t parity = 0;   // a bit per stage
   int stage = 0;
   bool ok = true;
-  for (; now.token < a.n_tokens; now.next(per, every)) {
+  for (; now.left > 0; now.next(per, step)) {
     // the load two pieces ahead takes the stage of two pieces ago, whose
     // store has been read out once at most the last one is pending
     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
     __syncwarp();
     load(ahead, (stage + 2) % kStages);
-    ahead.next(per, every);
-    if (now.c == 0) {
+    ahead.next(per, step);
+    if (now.c == 0 || !turned) {
+      turned = true;
       angles.set<sizeof(T) == 4>(at, phase, pos, a.mscale);
-      const int64_t next = now.token + every;
+      const int64_t next = now.token + step;
       if (a.rot > 0 && next < a.n_tokens) pos = __ldg(a.pos + next);
     }
     const bool is_q = now.c < cq;
@@ -208,16 +230,22 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) rope_stream_kernel(const
 template <typename T, int D>
 cudaError_t run_rope(RopeArgs a, const LaunchCtx& c) {
   constexpr int RPW = 32 / (D / 8);
-  // Bulk copies pay from about four pieces per warp on.
+  // Bulk copies pay from two pieces per warp on (2000 tokens of 40 heads, d = 128,
+  // bf16: 15.7 us straight, 11.5 streamed), from three where a token has only
+  // one or two, since each run of a token computes its angles (4000 tokens of 16
+  // heads, d = 64, bf16, 2.3 pieces per warp: 7.4 and 8.4 us).
   constexpr int CH = kStageBytes / (D * static_cast<int>(sizeof(T)));
-  const int64_t pieces = static_cast<int64_t>(a.n_tokens) * ((a.h_q + CH - 1) / CH + (a.h_kv + CH - 1) / CH);
-  if (pieces >= kStreamFrom * static_cast<int64_t>(c.sm_count) * kStreamWarps) {
+  const int per = (a.h_q + CH - 1) / CH + (a.h_kv + CH - 1) / CH;   // pieces per token
+  const int64_t warps = static_cast<int64_t>(c.sm_count) * kStreamWarps;
+  if (static_cast<int64_t>(a.n_tokens) * per >= (per > 2 ? 2 : 3) * warps) {
     const cudaError_t e =
         cudaFuncSetAttribute(rope_stream_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (static_cast<int64_t>(a.n_tokens) + kStreamWarps - 1) / kStreamWarps;
-    rope_stream_kernel<T, D><<<static_cast<unsigned>(blocks < c.sm_count ? blocks : c.sm_count), kStreamWarps * 32,
-                               kStreamSmem, c.stream>>>(a);
+    // whole tokens per warp leave a round part empty, even runs of pieces do not
+    // (4000 tokens of 40 heads: 26.7 and 18.1 us); but with many the runs are slower
+    // (32000: 110 and 126 us)
+    a.even = a.n_tokens < kEvenBelow * warps;
+    rope_stream_kernel<T, D><<<c.sm_count, kStreamWarps * 32, kStreamSmem, c.stream>>>(a);
     note_launch();
     return cudaGetLastError();
   }
@@ -230,7 +258,7 @@ cudaError_t run_rope(RopeArgs a, const LaunchCtx& c) {
   a.per_run = static_cast<int32_t>((groups + runs - 1) / runs);
   a.runs = (groups + a.per_run - 1) / a.per_run;
   const int64_t items = static_cast<int64_t>(a.n_tokens) * a.runs;
-  const int64_t most = static_cast<int64_t>(c.sm_count) * (sizeof(T) == 2 ? 4 : 3);   // blocks that run at a time
+  const int64_t most = static_cast<int64_t>(c.sm_count) * kDirect;   // blocks that run at a time
   const int64_t grid = (items + 7) / 8 < most ? (items + 7) / 8 : most;
   rope_kernel<T, D><<<static_cast<unsigned>(grid), 256, 0, c.stream>>>(a);
   note_launch();

@@ -174,46 +174,6 @@ __device__ __forceinline__ void scale_row(float (&x)[8], float f) {
   for (int i = 0; i < 8; i += 2) unpair(mul2(pair(x[i], x[i + 1]), pair(f, f)), x[i], x[i + 1]);
 }
 
-// A position's rotation with the weights of a head's dims folded in:
-// y[i] = x[i] * c[i] + x[partner of i] * s[i].
-struct Turn {
-  float c[8], s[8];
-
-  __device__ __forceinline__ void set(const LaneDims& at, const Angles& g, const float (&w)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // the pair's two places among the lane's eight dims
-      const int u = i, v = i + 4, p = 2 * i, q = 2 * i + 1;
-      if (at.half) {
-        c[u] = g.c[i] * w[u];
-        s[u] = -g.s[i] * w[v];
-        c[v] = g.c[i] * w[v];
-        s[v] = g.s[i] * w[u];
-      } else {
-        c[p] = g.c[i] * w[p];
-        s[p] = -g.s[i] * w[q];
-        c[q] = g.c[i] * w[q];
-        s[q] = g.s[i] * w[p];
-      }
-    }
-  }
-
-  // y = r * (x turned), r the norm's factor.  A dim that does not turn takes
-  // nothing from its neighbour, infinities neither.
-  __device__ __forceinline__ void apply(const LaneDims& at, const float (&x)[8], float r, float (&y)[8]) const {
-    if (!at.rotated) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i] * c[i] * r;
-    } else if (at.half) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i ^ 4], s[i], x[i] * c[i]) * r;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i ^ 1], s[i], x[i] * c[i]) * r;
-    }
-  }
-};
-
 // 1 / sqrt(mean(x^2) + eps) over the LPR lanes of a row.
 template <int LPR>
 __device__ __forceinline__ float norm_factor(const float (&x)[8], float eps) {

@@ -117,7 +117,10 @@ def test_rope_many_tokens_and_far_positions():
 
 @pytest.mark.parametrize("dtype,d,rot,layout,hq,hkv,T", [
     ("bf16", 128, 128, "half", 32, 8, 2600), ("bf16", 64, 32, "pairs", 33, 1, 3000), ("f32", 128, 96, "half", 9, 3, 3001),
-    ("f32", 64, 64, "pairs", 5, 17, 2500), ("bf16", 128, 0, "half", 1, 1, 4000)])
+    ("f32", 64, 64, "pairs", 5, 17, 2500), ("bf16", 128, 0, "half", 1, 1, 4000),
+    # runs of pieces that end inside a token, and whole tokens per warp
+    ("bf16", 128, 128, "half", 17, 3, 1800), ("bf16", 128, 0, "half", 1, 1, 6000),
+    ("bf16", 128, 128, "half", 2, 1, 14300), ("f32", 64, 48, "pairs", 9, 1, 14500)])
 def test_rope_of_many_tokens(dtype, d, rot, layout, hq, hkv, T):
     """Enough tokens for the streaming kernel, ragged numbers of heads per
     piece, in place too: sampled tokens against the oracle, every token

@@ -233,9 +233,10 @@ __device__ __forceinline__ void append_head(const AppendCfg& a, const AppendUnit
 // (no barrier but the one of the maximum).  64K tokens of eight heads: a block per
 // kv-head took 205 us, most of it the chain of index loads; the next head
 // alone on its way 115 us, bound by the bytes in flight; now 92 us, 66% of the
-// copy rate, at half of the issue slots with 16 warps per SM (registers).
+// copy rate, at half of the issue slots with 16 warps per SM (registers; at d = 64
+// four blocks of 128 threads for 16 warps: 67 us with two, 48 with four).
 template <typename T, int D, int P>
-__global__ void __launch_bounds__(P * D / 8 / kKeep, P * D / 8 / kKeep > 256 ? 1 : 2) append_kernel(const AppendCfg a) {
+__global__ void __launch_bounds__(P * D / 8 / kKeep, 512 / (P * D / 8 / kKeep)) append_kernel(const AppendCfg a) {
   constexpr int LPR = D / 8, KEEP = kKeep, THREADS = P * LPR / KEEP, ROWS = THREADS / LPR;
   constexpr int STAGES = page_stages<T>();
   __shared__ float red[2][THREADS / 32];

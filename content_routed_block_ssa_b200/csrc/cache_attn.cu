@@ -635,7 +635,10 @@ Split split_of(const ssa_cache_attn_params& p) {
   // One wave of the blocks that run at a time when the units are few, down to
   // one piece per warp (a latency: a sequence of 1000 took 14 us at four pieces
   // per warp, 10 at one); else about four waves, so that ragged lengths even
-  // out, with at least four pieces per warp.
+  // out, with at least eight pieces per warp of the longest axis (16 sequences
+  // of up to 4000, five drafts: 68 us at four, 54 at eight), four of selected
+  // blocks or where eight would leave SMs idle (8 sequences of five drafts,
+  // d = 64: 32 us at eight, 23 at four).
   const int64_t room = kBlocks * kSmCount;
   int64_t n = 1;
   if (s.units * 8 < room) {
@@ -652,7 +655,10 @@ Split split_of(const ssa_cache_attn_params& p) {
         if (c < cost) { cost = c; n = k; }
       }
     }
-    if (n > pieces / (4 * kWarps)) n = pieces / (4 * kWarps);
+    int64_t most = pieces / ((sel ? 4 : 8) * kWarps), fill = room / s.units;
+    if (fill > pieces / (4 * kWarps)) fill = pieces / (4 * kWarps);
+    if (most < fill) most = fill;
+    if (n > most) n = most;
   }
   s.splits = static_cast<int>(n < 1 ? 1 : n);
   return s;

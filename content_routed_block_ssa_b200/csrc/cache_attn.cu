@@ -24,9 +24,13 @@
 //    (O^T) and calls them its indexes; for O^T, bytes of two keys are paired
 //    by byte permutes before the conversion.
 //  * a page's key scale multiplies its logits; its value scale 2^e is added to
-//    the base-2 logits: P' = 2^(s + e - M), M the running maximum of s + e,
-//    is at most 1, fits float16 and needs no factor on the output, and the sum
-//    of the softmax takes P' 2^-e.
+//    the base-2 logits: P' = 2^(s + e - M) needs no factor on the output, and
+//    the sum of the softmax takes P' 2^-e.  The reference M is the running
+//    maximum of s + e less 15 (reference_of): P' is at most 2^15, float16's
+//    upper end, so that it keeps its 11 bits down to 2^-29 of the row's largest
+//    P' and vanishes below 2^-40.  (Relative to the maximum itself a key 2^-26
+//    below it left the output and stayed in the sum: rows that a key with a value of
+//    zero dominates by 18 nats came out as 0, whatever their other keys.)
 //  * queries become float16 after scaling each row by a power of two to a
 //    largest element in [2^14, 2^15): exact down to 2^-29 of the largest.
 #include <cuda_bf16.h>
@@ -56,7 +60,7 @@ struct CacheCfg {
   int32_t splits;
   float scale_log2;
   float* part_o;     // [units][splits][rows][D]
-  float2* part_ml;   // [units][splits][rows]: running maximum, sum
+  float2* part_ml;   // [units][splits][rows]: reference, sum
   uint32_t* err;
 };
 
@@ -124,6 +128,11 @@ __device__ __forceinline__ float load_query(const __nv_bfloat16* q, int t, bool 
     for (int i = 0; i < 8; ++i) h[c][i] = half2_bits(x[c][2 * i] * f, x[c][2 * i + 1] * f);
   return scale_log2 * pow2(e - 14);
 }
+
+// The reference of the base-2 logits up to m: 15 below it.  Not where float32
+// steps are so coarse that m - 15 could round to m - 16 and P' pass float16's
+// end; there m itself.  -inf (no keys yet) stays.
+__device__ __forceinline__ float reference_of(float m) { return fabsf(m) < 4194304.f ? m - 15.f : m; }
 
 // What a lane keeps of one upcoming piece of its warp.
 struct Piece {
@@ -375,8 +384,12 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
           for (int c = 0; c < 2; ++c) m[n][c] = fmaxf(m[n][c], __shfl_xor_sync(0xFFFFFFFFu, m[n][c], o));
       bool moved = false;
 #pragma unroll
-      for (int n = 0; n < R; ++n) moved = moved || m[n][0] > M[n][0] || m[n][1] > M[n][1];
-      if (__any_sync(0xFFFFFFFFu, moved)) {   // a maximum moved: rescale
+      for (int n = 0; n < R; ++n) {
+        m[n][0] = reference_of(m[n][0]);
+        m[n][1] = reference_of(m[n][1]);
+        moved = moved || m[n][0] > M[n][0] || m[n][1] > M[n][1];
+      }
+      if (__any_sync(0xFFFFFFFFu, moved)) {   // a reference moved: rescale
 #pragma unroll
         for (int n = 0; n < R; ++n) {
           float x[2];

@@ -586,7 +586,9 @@ SSA_API size_t ssa_cache_attn_workspace_size(const ssa_cache_attn_params* p);
  * lse = -inf.  Keys that a row does not attend have no part in it, NaN among
  * them.  kv_len below 0 counts as 0; beyond max_pages * page it is cut to
  * that.  Logits, softmax and sums are float32; the probabilities enter
- * the second product as float16, relative to the row's running maximum.
+ * the second product as float16: a key's probability times its page's value
+ * scale keeps 11 bits down to 2^-29 of the row's largest such product and
+ * leaves O below 2^-40 of it (and lse below 2^-141).
  * Meant for few new tokens (decode, drafts): with topk = 0 every 16 rows of
  * tokens x query heads of a kv-head read the sequence's cache once.
  *   Q          device [n_seq, n_q, h_q, d] bf16

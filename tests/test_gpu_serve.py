@@ -614,6 +614,142 @@ def test_cache_attention_scales_and_queries_of_very_different_size():
     check_cache(o, lse, q * 0, lens, table, codes, scale, page)
 
 
+# Per row and dim, against the row's own sum p|v| / sum p.  float16 keeps a
+# probability to 2^-11 of itself where p times the page's scale is above 2^-29
+# of the row's largest such product, which these cases stay within; 2^-11 more
+# is left for ex2.approx (2^-22) and float32 sums (n 2^-24).
+
+def check_cache_rows(o, lse, q, lens, table, codes, scale, page, idx=None, window=0, sm_scale=None):
+    args = (scale[0], scale[1], 1 / math.sqrt(q.shape[-1]) if sm_scale is None else sm_scale, idx, window)
+    ro, rl = S.cache_attention(f64(q), table, lens, page, codes[0], codes[1], *args)
+    ra, _ = S.cache_attention(f64(q), table, lens, page, codes[0], codes[1] & 0x7F, *args)
+    assert (np.abs(f64(o) - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * ra).all()
+    assert (np.abs(f64(lse) - rl) <= 2.0 ** -17 * (1 + np.abs(rl))).all()
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128)])
+@pytest.mark.parametrize("h_kv,G,n_q,topk", [(2, 4, 1, 0), (1, 8, 3, 0), (1, 4, 2, 4), (1, 12, 1, 4)])
+@pytest.mark.parametrize("nats", [4, 17, 18, 20])
+def test_cache_attention_beside_a_key_that_dominates(d, page, h_kv, G, n_q, topk, nats):
+    """One key far above the others with a value of zero: all of a row's output
+    comes from the others."""
+    r = rng_of("sink", d, h_kv, G, n_q)
+    lens, sink = [1000], 37
+    table, codes, scale, q, idx = cache_case(r, lens, n_q, h_kv, G, d, page, topk)
+    if topk:
+        idx[..., :] = [0, 2, 4, 5]                             # the dominating key's block among them
+    codes[0] = 0
+    codes[0, table[0, 0], :, sink, 0] = S.to_e4m3(1.0)
+    codes[1] = S.to_e4m3(100 + 50 * r.normal(size=codes[1].shape))
+    codes[1, table[0, 0], :, sink] = 0
+    scale[0], scale[1] = 1.0, 2.0 ** -7
+    q.zero_()
+    q[..., 0] = nats
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, idx, 64 if topk else 0, 1.0)
+    check_cache_rows(o, lse, q, lens, table, codes, scale, page, idx, 64 if topk else 0, 1.0)
+
+
+@pytest.mark.parametrize("d,page,G", [(128, 64, 4), (64, 128, 16)])
+@pytest.mark.parametrize("n_seq", [1, 600])
+def test_cache_attention_of_128k_keys_beside_a_key_that_dominates(d, page, G, n_seq):
+    """The same over an axis of many splits, or (sequences that share their
+    pages) of few long ones, and every one of its keys counted."""
+    r = rng_of("sink128k", d)
+    n = (1 << 17) + 77
+    pages = -(-n // page)
+    table, scale = r.permutation(pages)[None], np.ones((2, pages, 1))
+    scale[1] = 4.0
+    codes = np.zeros((2, pages, 1, page, d), np.uint8)
+    v = S.to_e4m3(100 + 50 * r.normal(size=(n, d)))
+    at = table[0, np.arange(n) // page], 0, np.arange(n) % page
+    codes[1][at] = v
+    sink = 70001
+    codes[0][table[0, sink // page], 0, sink % page, 0] = S.to_e4m3(1.0)
+    codes[1][table[0, sink // page], 0, sink % page] = 0
+    q = torch.zeros(n_seq, 1, G, d, device="cuda", dtype=torch.bfloat16)
+    val = 4.0 * S.e4m3_values()[codes[1][at]]
+    for nats in (17, 18, 0):
+        q[..., 0] = nats
+        o, lse, _ = run_cache(q, [n] * n_seq, np.repeat(table, n_seq, 0), codes, scale, page, sm_scale=1.0)
+        total = n - 1 + math.exp(nats)
+        ro, ra = val.sum(0) / total, np.abs(val).sum(0) / total
+        assert (np.abs(f64(o) - ro) <= 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * ra).all()
+        # at 0 nats the sum is a whole number times a power of two, exact but for ex2.approx's common factor
+        # (2^-22), and 2^30 in all: log2f is off by one unit of 2^-19 at most, adding the reference by half
+        # of one, times ln 2, and that product by 2^-21: 0.64 of 2^-18, and one key is 2^-17
+        assert (np.abs(f64(lse) - math.log(total)) <= (2.0 ** -18 if nats == 0 else 2.0 ** -17 * (1 + nats))).all()
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128), (128, 128), (64, 64)])
+@pytest.mark.parametrize("h_kv,G,n_q,topk", [(2, 4, 1, 0), (1, 8, 3, 0), (2, 4, 2, 16), (1, 12, 1, 16)])
+def test_cache_attention_counts_every_key(d, page, h_kv, G, n_q, topk):
+    """Equal logits and a value of 1 in dim j % d alone: dim c counts the
+    attended keys j = c (mod d), and the log-sum-exp all of them."""
+    r = rng_of("count", d, page, h_kv, G, n_q)
+    lens = [3000, 4096, 1501]
+    table, codes, scale, q, idx = cache_case(r, lens, n_q, h_kv, G, d, page, topk)
+    window = 150 if topk else 0
+    codes[1] = 0
+    for s, L in enumerate(lens):
+        j = np.arange(L)
+        codes[1, table[s, j // page], :, j % page, j % d] = S.to_e4m3(1.0)
+    scale[1] = 1.0
+    q.zero_()
+    o, lse, p = run_cache(q, lens, table, codes, scale, page, idx, window)
+    assert topk or ssa.ssa_cache_attn_workspace_size(p) > 0
+    o, lse = f64(o), f64(lse)
+    for s, L in enumerate(lens):
+        for i in range(n_q):
+            pos = L - n_q + i
+            for h in range(h_kv * G):
+                keys = np.arange(pos + 1)
+                if topk:
+                    used, _ = S.used_blocks(idx[s, i, h // G], pos, page)
+                    keys = keys[np.isin(keys // page, used) | (keys > pos - window)]
+                n = len(keys)
+                want = np.bincount(keys % d, minlength=d) / n
+                # one key more or less is at least 1/64 of a dim's count
+                assert (np.abs(o[s, i, h] - want) <= (2.0 ** -8 + 2.0 ** -10) * want).all()
+                assert abs(lse[s, i, h] - math.log(n)) <= 2.0 ** -16          # one key is 2^-12
+
+
+def test_cache_attention_beside_a_page_of_far_larger_values():
+    """A page whose value scale is 2^26 times the others' and whose codes are
+    zero in half of the dims: there the other pages' values count in full."""
+    r = rng_of("bigpage")
+    d, page, lens = 128, 128, [500] * 40                       # one split: a warp meets the page and others
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 2, 4, d, page)
+    scale[1] = 2.0 ** -8
+    scale[1, table[:, 2]] = 2.0 ** 18
+    codes[1, table[:, 2], :, :, ::2] = 0
+    for factor in (0.0, 1.0):
+        o, lse, _ = run_cache(q * factor, lens, table, codes, scale, page, sm_scale=2.0 ** -12)
+        check_cache_rows(o, lse, q * factor, lens, table, codes, scale, page, sm_scale=2.0 ** -12)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 18, 2.0 ** 22, 2.0 ** 24, 2.0 ** 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_cache_attention_of_logits_past_float32_steps(size, sign):
+    """Logits whose float32 steps are 1 and more: the largest key takes the row."""
+    r = rng_of("huge", size)
+    d, page, lens = 64, 64, [900]
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 1, 4, d, page)
+    scale[0], scale[1] = 1.0, 2.0 ** -7
+    codes[0] = 0
+    rank = r.permutation(900)
+    j = np.arange(900)
+    codes[0, table[0, j // page], 0, j % page, 0] = np.where(rank < 800, 0x38 + rank % 40, 0x38 + 50)   # 1 .. 30, 80
+    best = 417
+    codes[0, table[0, best // page], 0, best % page, 0] = S.to_e4m3(112.0) if sign > 0 else S.to_e4m3(0.5)
+    q.zero_()
+    q[..., 0] = sign * size
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page, sm_scale=1.0)
+    want = S.e4m3_values()[codes[1, table[0, best // page], 0, best % page]] * scale[1, 0, 0]
+    assert (np.abs(f64(o) - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all()
+    logit = sign * size * (112.0 if sign > 0 else 0.5)
+    assert (np.abs(f64(lse) - logit) <= 2.0 ** -17 * abs(logit)).all()
+
+
 # ---------------------------------------------------------------- packed prompts
 
 def run_prompt(q, k, v, qs, ks, sm_scale=None, lse=True, stream=None):

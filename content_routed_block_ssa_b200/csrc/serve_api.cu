@@ -69,8 +69,9 @@ ssa_status check_cache_attn(const ssa_cache_attn_params* p) {
   if (st != SSA_OK) return st;
   if (p->h_q % p->h_kv != 0 || (p->topk == 0) != (p->window == 0)) return SSA_ERR_INVALID_ARG;
   if (p->h_q / p->h_kv > 16 || p->topk > 32 || p->window > 4032) return SSA_ERR_UNSUPPORTED;
-  // rows and blocks are counted in 32 bits
-  if (static_cast<int64_t>(p->n_seq) * p->n_q * p->h_q > (INT32_MAX >> 1)) return SSA_ERR_UNSUPPORTED;
+  // rows and blocks are counted in 32 bits (one product at a time: three would pass 64)
+  const int64_t rows = static_cast<int64_t>(p->n_q) * p->h_q;
+  if (rows > (INT32_MAX >> 1) || rows * p->n_seq > (INT32_MAX >> 1)) return SSA_ERR_UNSUPPORTED;
   return SSA_OK;
 }
 

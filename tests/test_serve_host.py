@@ -126,6 +126,18 @@ def test_cache_attn_refusals(kw, code):
     assert ssa.ssa_launch_count() == before
 
 
+@pytest.mark.parametrize("kw", [dict(n_seq=2 ** 31 - 1, n_q=2 ** 31 - 1, h_q=4, h_kv=4),   # past 64 bits together
+                                dict(n_seq=2 ** 31 - 1, n_q=2 ** 31 - 1, h_q=16, h_kv=1, topk=4, window=64),
+                                dict(n_seq=1 << 30, n_q=1 << 30, h_q=16, h_kv=16), dict(n_seq=2 ** 31 - 1),
+                                dict(n_seq=1, n_q=2 ** 31 - 1), dict(n_seq=1 << 29, n_q=1, h_q=4, h_kv=4)])
+def test_cache_attn_refuses_more_rows_than_it_counts(kw):
+    before = ssa.ssa_launch_count()
+    p = cache(**kw)
+    assert ssa.ssa_cache_attn_workspace_size(p) == 0
+    assert call_cache(p) == UNSUPPORTED
+    assert ssa.ssa_launch_count() == before
+
+
 def test_cache_attn_pointers_and_workspace():
     p = cache()
     for n in ("Q", "table", "len", "kc", "vc", "ks", "vs", "O"):

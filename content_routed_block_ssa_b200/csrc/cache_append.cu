@@ -394,8 +394,7 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
 
 template <typename T, int D, int P>
 cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
-  const int64_t units = a.n_tokens / P + 2 * static_cast<int64_t>(a.n_seq);
-  if (units > INT32_MAX || units * a.h_kv > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t units = a.n_tokens / P + 2 * static_cast<int64_t>(a.n_seq);   // below 2^27, times h_kv below 2^31
   a.n_units = static_cast<int32_t>(units);
   if (a.n_tokens <= a.n_seq) {
     append_few_kernel<T, D, P><<<static_cast<unsigned>((units * 2 * a.h_kv + 7) / 8), 256, 0, c.stream>>>(a);
@@ -410,8 +409,7 @@ cudaError_t run_append(AppendCfg a, const LaunchCtx& c) {
   if (runs > a.h_kv) runs = a.h_kv;
   a.per_run = static_cast<int32_t>((a.h_kv + runs - 1) / runs);
   a.runs = (a.h_kv + a.per_run - 1) / a.per_run;
-  const int64_t grid = units * a.runs * 2;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t grid = units * a.runs * 2;   // several runs only with fewer units than SMs
   const cudaError_t e = cudaFuncSetAttribute(append_kernel<T, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   append_kernel<T, D, P><<<static_cast<unsigned>(grid), kThreads, kSmem, c.stream>>>(a);

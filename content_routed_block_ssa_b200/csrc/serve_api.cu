@@ -58,6 +58,8 @@ ssa_status check_append(const ssa_append_params* p) {
   if (bad_stride(p->k_stride, p->h_kv, p->d, es) || bad_stride(p->v_stride, p->h_kv, p->d, es))
     return SSA_ERR_INVALID_ARG;
   if (p->n_seq > (1 << 24)) return SSA_ERR_UNSUPPORTED;
+  // pages that the tokens may touch, times kv-heads: the launch counts them in 32 bits
+  if ((p->n_tokens / p->page + 2 * static_cast<int64_t>(p->n_seq)) * p->h_kv > INT32_MAX) return SSA_ERR_UNSUPPORTED;
   return SSA_OK;
 }
 

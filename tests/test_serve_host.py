@@ -85,6 +85,14 @@ def test_append_refusals(kw, code):
     assert ssa.ssa_launch_count() == before
 
 
+@pytest.mark.parametrize("kw", [dict(n_seq=1 << 24, h_kv=128), dict(n_seq=1 << 24, h_kv=65535),
+                                dict(n_tokens=2 ** 31 - 1, h_kv=64), dict(n_tokens=2 ** 31 - 1, n_seq=1 << 24, page=128, h_kv=50)])
+def test_append_refuses_more_pages_of_heads_than_it_counts(kw):
+    before = ssa.ssa_launch_count()
+    assert call_append(append(**kw)) == UNSUPPORTED
+    assert ssa.ssa_launch_count() == before
+
+
 def test_append_pointers():
     p = append()
     for n in ("K", "V", "f", "cu", "have", "table", "kc", "vc", "ks", "vs"):

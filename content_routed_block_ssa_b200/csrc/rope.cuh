@@ -24,11 +24,19 @@
 
 namespace ssa {
 
-// Turns per position, 64-bit fixed point.
+// Turns per position, 64-bit fixed point: freq / (2 pi) modulo one to 2^-63 (for
+// |freq| below 2^38), from the rounded product and what it leaves: alone, its
+// rounding of 2^-53 times the frequency would grow with the position.  Adding
+// 3 * 2^51 rounds to a whole number in the sum's low bits, without the slow conversions.
 __device__ __forceinline__ uint64_t phase_of(double freq) {
-  double t = freq * 0.15915494309189535;   // 1 / (2 pi)
-  t -= floor(t);
-  return static_cast<uint64_t>(t * 18446744073709551616.0);   // saturates at one turn
+  constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;   // 1 / (2 pi) to 107 bits
+  constexpr double whole = 6755399441055744.0, two32 = 4294967296.0;
+  const double t = freq * hi, rest = fma(freq, lo, fma(freq, hi, -t));
+  const double x = (t - ((t + whole) - whole)) * two32;
+  const double u = x + whole;                                                        // the upper 32 bits
+  const double v = fma(rest, two32 * two32, (x - (u - whole)) * two32) + whole;      // the lower ones, signed
+  return (static_cast<uint64_t>(__double2loint(u)) << 32) +
+         static_cast<uint64_t>(__double_as_longlong(v) - __double_as_longlong(whole));
 }
 
 // cos and sin of position * frequency.  PRECISE: to float32's rounding;
@@ -62,6 +70,28 @@ struct LaneDims {
   __device__ __forceinline__ void phases(const double* freq, int sub, uint64_t (&phase)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) phase[i] = rotated ? phase_of(__ldg(freq + 4 * sub + i)) : 0;
+  }
+  // The same, each computed once per block (every thread calls).
+  __device__ __forceinline__ void block_phases(const double* freq, int rot, uint64_t (&all)[64], int sub,
+                                               uint64_t (&phase)[4]) const {
+    if (static_cast<int>(threadIdx.x) < rot / 2) all[threadIdx.x] = phase_of(__ldg(freq + threadIdx.x));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) phase[i] = rotated ? all[4 * sub + i] : 0;
+  }
+  // The same for a head of D dims, each computed once per warp (every lane calls).
+  template <int D>
+  __device__ __forceinline__ void warp_phases(const double* freq, int rot, int sub, uint64_t (&phase)[4]) const {
+    constexpr int N = D / 64;   // phases computed by a lane
+    const int lane = threadIdx.x & 31;
+    uint64_t own[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) own[k] = N * lane + k < rot / 2 ? phase_of(__ldg(freq + N * lane + k)) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t p = __shfl_sync(0xFFFFFFFFu, own[i % N], (4 * sub + i) / N & 31);
+      phase[i] = rotated ? p : 0;
+    }
   }
 };
 

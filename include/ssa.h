@@ -489,8 +489,8 @@ typedef struct {
  * (norm = 1), then every pair (a, b) of the first rot dims turns by
  * angle = position * freq[i]: (a, b) -> mscale (a cos - b sin, b cos + a sin).
  * Computed in float32 and rounded once.  Angles are reduced to one turn in
- * 64-bit fixed point, so far positions lose nothing; positions may be
- * negative.
+ * 64-bit fixed point (for |freq| below 2^38), so far positions lose nothing;
+ * positions may be negative.
  *   Q, K          strided device [n_tokens, h_q | h_kv, d] of dtype
  *   q_weight, k_weight  device float32 [d], may be NULL (ones); norm = 0
  *                 ignores them

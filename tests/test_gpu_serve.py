@@ -115,6 +115,62 @@ def test_rope_many_tokens_and_far_positions():
     assert (np.abs(f64(qo) - ref) <= U["f32"] * np.abs(ref) + (FUZZ["f32"] + 2.0 ** -20) * big).all()
 
 
+def turns(freq, pos):
+    """pos * freq / (2 pi) modulo one in exact arithmetic (freq is a float64)."""
+    from fractions import Fraction
+    two_pi = Fraction(62831853071795864769252867665590057683943387987502, 10 ** 49)
+    return float(Fraction(float(freq)) * int(pos) / two_pi % 1)
+
+
+@pytest.mark.parametrize("T", [40, 15000])   # straight, and streamed
+@pytest.mark.parametrize("fast", [3.0, 1000.0, 1e6])
+def test_rope_positions_lose_nothing(T, fast):
+    """Frequencies of up to `fast` radians at positions up to 2^31: the angle's
+    error does not grow with either (the float32 part is FUZZ, as above)."""
+    d = 64
+    r = rng_of("turns", fast)
+    x = dev(r.normal(size=(T, 1, d)), torch.float32)
+    f = torch.from_numpy(np.exp(r.uniform(np.log(fast) - 3, np.log(fast), size=d // 2)))
+    pos = r.integers(-(1 << 31), 1 << 31, size=T)
+    pos[:4] = [(1 << 31) - 1, -(1 << 31), 0, 1]
+    q, k = torch.empty_like(x), torch.empty_like(x)
+    p = ssa.make_rope_params(T, 1, 1, d, dtype="f32", norm=False)
+    ssa.ssa_qk_rope(p, x, x, None, None, f.cuda(), dev(pos, torch.int32), q, k)
+    ok()
+    assert torch.equal(q, k)
+    n = np.arange(40) if T == 40 else np.concatenate([[0, 1, 2, 3], r.integers(0, T, 60)])
+    a = np.array([[2 * math.pi * turns(g, t) for g in f] for t in pos[n]])
+    v = f64(x)[n, 0]
+    u, w = v[:, :d // 2], v[:, d // 2:]
+    ref = np.concatenate([u * np.cos(a) - w * np.sin(a), w * np.cos(a) + u * np.sin(a)], 1)
+    big = np.abs(v).max(-1, keepdims=True)
+    assert (np.abs(f64(q)[n, 0] - ref) <= U["f32"] * np.abs(ref) + FUZZ["f32"] * big).all()
+
+
+def test_appended_keys_turn_by_their_far_positions():
+    """The same for keys appended next to position 2^31."""
+    d, page, n = 64, 128, 100
+    r = rng_of("turnsapp")
+    width = (1 << 31) // page - 1
+    have = width * page - n
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, have // page:] = 0
+    x = dev(r.normal(size=(n, 1, d)), torch.float32)
+    f = torch.from_numpy(np.exp(r.uniform(11, 14, size=d // 2)))
+    kc, vc = (torch.zeros(1, 1, page, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((1, 1), 2.0 ** -40, device="cuda") for _ in range(2))
+    p = ssa.make_append_params(n, 1, width, 1, page, 1, d, dtype="f32", norm=False)
+    ssa.ssa_cache_append(p, x, x, None, f.cuda(), dev([0, n], torch.int32), dev([have], torch.int32), table, kc, vc, ks, vs)
+    ok()
+    a = np.array([[2 * math.pi * turns(g, have + t) for g in f] for t in range(n)])
+    v = f64(x)[:, 0]
+    u, w = v[:, :d // 2], v[:, d // 2:]
+    ref = np.concatenate([u * np.cos(a) - w * np.sin(a), w * np.cos(a) + u * np.sin(a)], 1)
+    s = float(ks)
+    got = S.e4m3_values()[kc.cpu().numpy()[0, 0, page - n:]] * s
+    assert (np.abs(got - ref) <= 2.0 ** -4 * np.abs(ref) + 2.0 ** -10 * s + 2.0 ** -16 * np.abs(v).max(-1, keepdims=True)).all()
+
+
 @pytest.mark.parametrize("dtype,d,rot,layout,hq,hkv,T", [
     ("bf16", 128, 128, "half", 32, 8, 2600), ("bf16", 64, 32, "pairs", 33, 1, 3000), ("f32", 128, 96, "half", 9, 3, 3001),
     ("f32", 64, 64, "pairs", 5, 17, 2500), ("bf16", 128, 0, "half", 1, 1, 4000),

@@ -44,7 +44,7 @@ struct PromptShape {
   static constexpr int TILE = 128 * ROW * HALVES;     // 128 rows (queries x heads, or keys)
   static constexpr int SLOTS = TILES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 5);   // ring of K and V tiles
   static constexpr int BARS = TILES * TILE + SLOTS * TILE;
-  static constexpr int NBAR = 1 + 2 * SLOTS + TILES + 2 * TILES + TILES + 1;
+  static constexpr int NBAR = 1 + 2 * SLOTS + TILES + 2 * TILES + TILES + TILES + 1;
   static constexpr int USED = BARS + NBAR * 8 + 16;
   static constexpr int SMEM = USED + 1024 < 232448 ? USED + 1024 : 232448;
   static constexpr int LOADER = 4 * TILES, ISSUER = LOADER + 1;   // warps: 4 softmax warps per tile, loads, products
@@ -60,11 +60,10 @@ struct PromptShape {
 };
 
 struct PromptArgs {
-  const __nv_bfloat16 *Q, *K, *V;   // for rows beside values that are not finite
   const int32_t *q_start, *kv_start;
   __nv_bfloat16* O;
   float* lse;
-  int64_t q_stride, k_stride, v_stride, o_stride;
+  int64_t o_stride;
   int32_t n_seq, n_q, n_kv, h_q, h_kv, G, qt;
   int32_t n_units;
   float scale_log2;
@@ -162,38 +161,62 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ bool not_finite2(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+// 0 * x + acc of bf16 pairs: stays a zero while x is finite.  (By tests of the
+// exponents the look over the values took 10 of 230 us of three packed prompts of 8192.)
+__device__ __forceinline__ uint32_t times0(uint32_t x, uint32_t acc) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0));
+  return acc;
 }
 
-// One row by a warp, without the tensor core: o of the row's own keys, from
-// its maximum reference (base-2) and sum.  For tiles where a value that some
-// rows do not attend is not finite (0 * inf is NaN in the product).
+// A step's P V without the tensor core, a row per thread: where a value that
+// some rows of the tile do not attend is not finite (0 * inf is NaN in the
+// product).  P in bf16 pairs at p_col, values at sV, keys up to the row's
+// `last`; o_col += the product (`first`: =).  Only a tile's last two steps may come
+// here, for up to 60 us each (a prompt of 8192, eight heads on one, d = 128, one
+// such value near its end: 116 us without, 174 with it).
 template <int D>
-__device__ void plain_row(const PromptArgs& a, const __nv_bfloat16* q, const PromptUnit& u, int kvh, int pos, float m2,
-                          float inv_l, __nv_bfloat16* out) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  float x[E], o[E];
+__device__ __forceinline__ void product_by_hand(uint32_t p_col, uint32_t o_col, const uint8_t* sV, int last, bool first) {
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 16) {
+    uint32_t o[16];
+    if (first) {   // the same for the tile
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = __bfloat162float(q[lane * E + e]);
-    o[e] = 0.f;
+      for (int k = 0; k < 16; ++k) o[k] = 0;
+    } else {
+      tmem_ld16(o_col + d0, o);
+      tmem_wait_ld();
+      tmem_regs_ready(o);
+    }
+    const uint8_t* half = sV + (d0 >> 6) * (128 * 128);
+    const int chunk = (d0 & 63) >> 3;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      if (__all_sync(0xFFFFFFFFu, c > last)) break;   // (P is not there in a short last step)
+      uint32_t p[16];
+      tmem_ld16(p_col + c / 2, p);
+      tmem_wait_ld();
+      tmem_regs_ready(p);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const uint8_t* row = half + (c + k) * 128;   // swizzled by the key's place among eight
+        const bool in = c + k <= last;
+        const float x = in ? __uint_as_float(k & 1 ? p[k / 2] & 0xFFFF0000u : p[k / 2] << 16) : 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + (((chunk + h) ^ (k & 7)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t y = in ? w[e] : 0;
+            uint32_t* to = o + 8 * h + 2 * e;
+            to[0] = __float_as_uint(fmaf(x, __uint_as_float(y << 16), __uint_as_float(to[0])));
+            to[1] = __float_as_uint(fmaf(x, __uint_as_float(y & 0xFFFF0000u), __uint_as_float(to[1])));
+          }
+        }
+      }
+    }
+    tmem_st16(o_col + d0, o);
   }
-  for (int j = 0; j <= pos; ++j) {
-    const __nv_bfloat16* k = a.K + static_cast<int64_t>(u.k_row + j) * a.k_stride + kvh * D + lane * E;
-    const __nv_bfloat16* v = a.V + static_cast<int64_t>(u.k_row + j) * a.v_stride + kvh * D + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], __bfloat162float(k[e]), s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
-    const float p = fast_exp2(fmaf(s, a.scale_log2, -m2));
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(p, __bfloat162float(v[e]), o[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane * E + e] = __float2bfloat16(o[e] * inv_l);
 }
 
 template <int D, int TILES>
@@ -222,18 +245,21 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
   uint64_t* s_full = empty + C::SLOTS;     // [tiles]
   uint64_t* p_full = s_full + TILES;       // [tiles][2 halves of the step's keys]
   uint64_t* o_full = p_full + 2 * TILES;   // [tiles] the tile's last product is done
-  uint64_t* mma_done = o_full + TILES;
+  uint64_t* hand_done = o_full + TILES;    // [tiles] a step's product added by the softmax warps
+  uint64_t* mma_done = hand_done + TILES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int32_t* odd_at = reinterpret_cast<int32_t*>(tmem_slot + 1);   // [tiles] 1 + the step to be added by hand
 
   // steps of each tile: keys 0 .. position of its last row; a last step that
   // needs no more than half of its 128 keys leaves out the rest
   const int off = u.kv_len - u.q_len;
-  int steps[TILES], n = 0;
+  int steps[TILES], masked_from[TILES], n = 0;   // masked_from: the first step with keys that some rows do not attend
   bool short_last[TILES];
 #pragma unroll
   for (int t = 0; t < TILES; ++t) {
     const int q_first = u.q0 + t * a.qt, last = min(q_first + a.qt, u.q_len) - 1 + off;
     steps[t] = q_first < u.q_len && last >= 0 ? last / 128 + 1 : 0;
+    masked_from[t] = max(q_first + off + 1, 0) / 128;
     short_last[t] = steps[t] > 0 && last % 128 < 64;
     n = max(n, steps[t]);
   }
@@ -257,6 +283,8 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
       mbar_init(&p_full[2 * t], 4);
       mbar_init(&p_full[2 * t + 1], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&hand_done[t], 4);
+      odd_at[t] = 0;
     }
     mbar_init(mma_done, 1);
     fence_barrier_init();
@@ -335,6 +363,7 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
         __syncwarp();
       }
       int v_slot = 1, v_use = 0;   // slot of load 2 j + 1 and the parity of its use
+      int hands[TILES] = {};       // steps added by hand
       for (int j = 0; j < n && ok; ++j) {
         const bool more = j + 1 < n;
         const int k_slot = v_slot + 1 == C::SLOTS ? 0 : v_slot + 1, k_use = k_slot == 0 ? v_use ^ 1 : v_use;   // load 2 j + 2
@@ -344,20 +373,33 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
           if (!ok) break;
           const bool brief = short_last[t] && j + 1 == steps[t];
           if (j < steps[t]) {
-            // the first half of the keys while the second is exponentiated
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && wait(&p_full[2 * t + h], j & 1);
+            bool by_hand = false;   // the softmax warps add this step's product themselves
+            if (j >= masked_from[t]) {
+              ok = ok && wait(&p_full[2 * t], j & 1);
+              by_hand = ok && __any_sync(0xFFFFFFFFu, odd_at[t] == j + 1);
+            }
+            if (by_hand) {
+              ok = wait(&hand_done[t], hands[t] & 1);
+              ++hands[t];
               tc_fence_after();
-              if (ok && leader) {
-                if (h == 0 || !brief)
-#pragma unroll
-                  for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                    umma_bf16_tmem_a(tmem_o + 128 * t, tmem + 128 * t + ks * 8,
-                                     v_desc + v_slot * kTile + ((ks * 16 * C::ROW) >> 4), IDESC_O, (j | ks) != 0);
-                if (h == 1 && j + 1 == steps[t]) umma_commit(&o_full[t]);
-              }
+              if (ok && leader && j + 1 == steps[t]) umma_commit(&o_full[t]);
               __syncwarp();
+            } else {
+              // the first half of the keys while the second is exponentiated
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                ok = ok && wait(&p_full[2 * t + h], j & 1);
+                tc_fence_after();
+                if (ok && leader) {
+                  if (h == 0 || !brief)
+#pragma unroll
+                    for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                      umma_bf16_tmem_a(tmem_o + 128 * t, tmem + 128 * t + ks * 8,
+                                       v_desc + v_slot * kTile + ((ks * 16 * C::ROW) >> 4), IDESC_O, (j | ks) != 0);
+                  if (h == 1 && j + 1 == steps[t]) umma_commit(&o_full[t]);
+                }
+                __syncwarp();
+              }
             }
           }
           if (t == TILES - 1 && leader) umma_commit(&empty[v_slot]);
@@ -393,9 +435,20 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
     const int pos_first = u.q0 + t * a.qt + off;            // of the tile's first row
     float m = -INFINITY;     // reference of the row, in logits before the scale
     uint64_t l2[2] = {0, 0};
-    bool odd = false;        // a value that some rows do not attend is not finite
     bool ok = true;
-    for (int j = 0; j < my_steps; ++j) {
+    // a barrier of the tile's four warps
+    const auto tile_any = [&](bool x) {
+      int any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+          "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"(x ? 1 : 0), "r"(1 + t)
+          : "memory");
+      return any != 0;
+    };
+    int j = 0;
+    for (; j < my_steps; ++j) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[t], j & 1, a.err, SITE_PROMPT_SOFTMAX));
       if (!ok) break;
       tc_fence_after();
@@ -453,17 +506,19 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
         if (!ok) break;
         uint8_t* sV = ring + (i % C::SLOTS) * C::TILE;
         const int end = min(u.kv_len - j * 128, 128), from = max(pos_first + 1 - j * 128, 0);
-        for (int x = row; x < (128 - from) * 8 * C::HALVES; x += 128) {
-          const int key = from + x / (8 * C::HALVES), c = x % (8 * C::HALVES);
-          uint4* w = reinterpret_cast<uint4*>(sV + (c >> 3) * 128 * C::ROW + key * C::ROW + (c & 7) * 16);
-          if (key >= end) {
-            *w = make_uint4(0, 0, 0, 0);
-          } else {
-            const uint4 v = *w;
-            odd |= not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
-          }
+        constexpr int CH = 8 * C::HALVES;   // 16-byte pieces of a key
+        const auto piece = [&](int x) {
+          return reinterpret_cast<uint4*>(sV + (x % CH >> 3) * 128 * C::ROW + x / CH * C::ROW + (x & 7) * 16);
+        };
+        for (int x = end * CH + row; x < 128 * CH; x += 128) *piece(x) = make_uint4(0, 0, 0, 0);
+        uint32_t odd = 0;
+#pragma unroll 4
+        for (int x = from * CH + row; x < end * CH; x += 128) {
+          const uint4 v = *piece(x);
+          odd = times0(v.w, times0(v.z, times0(v.y, times0(v.x, odd))));
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (odd & 0x7FFF7FFFu) odd_at[t] = j + 1;   // one is not finite
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -487,15 +542,18 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
       }
+      // (after P has left: the tensor core need not wait for this barrier)
+      if (masked && tile_any(odd_at[t] == j + 1)) {
+        product_by_hand<D>(s_col, o_col, ring + ((2 * j + 1) % C::SLOTS) * C::TILE, pos - j * 128, j == 0);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hand_done[t]);
+      }
     }
-    // whether any warp of the tile saw such a value (a barrier of its four warps)
-    int any_odd = 0;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-        : "=r"(any_odd)
-        : "r"(odd ? 1 : 0), "r"(1 + t)
-        : "memory");
+    // a warp that gave up before the barrier of step j still meets the others there and after
+    for (; j < my_steps; ++j)
+      if (j * 128 + 127 > pos_first) tile_any(false);
     float l0, l1, l2_, l3;
     unpair(l2[0], l0, l1);
     unpair(l2[1], l2_, l3);
@@ -509,38 +567,26 @@ __global__ void __launch_bounds__(PromptShape<D, TILES>::THREADS, PromptShape<D,
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], 0, a.err, SITE_PROMPT_SOFTMAX));
     if (ok) {
       if (valid && a.lse) a.lse[q_row * a.h_q + head] = l == 0.f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
-      if (any_odd) {
-        const uint32_t vm = __ballot_sync(0xFFFFFFFFu, valid);
-        for (int k = 0; k < 32; ++k) {
-          if (!((vm >> k) & 1u)) continue;
-          const int64_t qr = __shfl_sync(0xFFFFFFFFu, q_row, k);
-          const int hd = __shfl_sync(0xFFFFFFFFu, head, k);
-          plain_row<D>(a, a.Q + qr * a.q_stride + static_cast<int64_t>(hd) * D, u, kvh,
-                       __shfl_sync(0xFFFFFFFFu, pos, k), __shfl_sync(0xFFFFFFFFu, mr, k),
-                       __shfl_sync(0xFFFFFFFFu, inv, k), a.O + qr * a.o_stride + static_cast<int64_t>(hd) * D);
-        }
-      } else {
-        tc_fence_after();
+      tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (my_steps > 0) {   // the same for the tile
-            tmem_ld32(o_col + 32 * c, o);
-            tmem_wait_ld();
-            tmem_regs_ready(o);
-          } else {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (my_steps > 0) {   // the same for the tile
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_wait_ld();
+          tmem_regs_ready(o);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
-          }
-          if (valid) {
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if (valid) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-              reinterpret_cast<uint4*>(out)[c * 4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+            reinterpret_cast<uint4*>(out)[c * 4 + k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
@@ -576,13 +622,10 @@ cudaError_t launch_prompt_attn(const ssa_prompt_params& p, const void* Q, const 
                                const int32_t* q_start, const int32_t* kv_start, void* O, float* lse,
                                const LaunchCtx& c) {
   PromptArgs a{};
-  a.Q = static_cast<const __nv_bfloat16*>(Q);
-  a.K = static_cast<const __nv_bfloat16*>(K);
-  a.V = static_cast<const __nv_bfloat16*>(V);
   a.q_start = q_start; a.kv_start = kv_start;
   a.O = static_cast<__nv_bfloat16*>(O);
   a.lse = lse;
-  a.q_stride = p.q_stride; a.k_stride = p.k_stride; a.v_stride = p.v_stride; a.o_stride = p.o_stride;
+  a.o_stride = p.o_stride;
   a.n_seq = p.n_seq; a.n_q = p.n_q; a.n_kv = p.n_kv; a.h_q = p.h_q; a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;
   a.qt = 128 / a.G;

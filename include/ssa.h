@@ -629,8 +629,9 @@ typedef struct {
  * A row without keys gives O = 0 and lse = -inf.  Rows of Q, K and V outside
  * every sequence are not part of any result and their rows of O and lse stay
  * as they were.  Keys that a row does not attend have no part in it,
- * infinities and NaN among them.  Logits, softmax and sums are float32; the
- * probabilities enter the second product as bf16.
+ * infinities and NaN among them (such a value costs the rows around it up to
+ * 0.1 ms).  Logits, softmax and sums are float32; the probabilities enter the
+ * second product as bf16.
  *   Q          strided device [n_q, h_q, d] bf16
  *   K, V       strided device [n_kv, h_kv, d] bf16
  *   q_start, kv_start  device int32 [n_seq + 1], non-decreasing, within

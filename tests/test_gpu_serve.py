@@ -927,6 +927,66 @@ def test_prompt_ignores_what_a_row_does_not_attend():
     assert torch.equal(o[~o.isnan()], clean[~o.isnan()])
 
 
+@pytest.mark.parametrize("d,h_kv,G", [(128, 1, 4), (64, 1, 8), (128, 40, 4), (64, 60, 4), (64, 40, 7), (128, 20, 16)])
+@pytest.mark.parametrize("more", [0, 300])   # keys before the prompt
+def test_prompt_of_values_that_are_not_finite(d, h_kv, G, more):
+    """Infinities and NaN among a sequence's values, in one-tile and two-tile
+    blocks: rows behind them show them in their own dims, all others are the
+    oracle's as closely as ever."""
+    r = rng_of("podd", d, h_kv, G, more)
+    lens = [700, 150, 5]
+    q, k, v, qs, ks = prompt_case(r, lens, [n + more for n in lens], h_kv, G, d)
+    pick = sorted({0, h_kv // 2, h_kv - 1})
+    v = v.clone()
+    odd = [math.inf, -math.inf, math.nan]
+    at = [0, 1, 63, 64, 130, 333, 334, 511, 639, 640, 698, 699, 700, 849]   # of the first two sequences' rows
+    for i, row in enumerate(at):
+        s = int(row >= 700)
+        key = row - 700 * s + (int(ks[s + 1] - ks[s]) - lens[s] if i % 2 else 0) + int(ks[s])
+        v[key, pick[i % len(pick)], (7 * i) % d] = odd[i % 3]
+    o, lse = run_prompt(q, k, v, qs, ks)
+    hd = [g * G + i for g in pick for i in range(G)]
+    qn, kn, vn, o, lse = f64(q[:, hd]), f64(k[:, pick]), f64(v[:, pick]), f64(o[:, hd]), f64(lse[:, hd])
+    with np.errstate(invalid="ignore"):
+        ro, rl = S.prompt_attention(qn, kn, vn, qs, ks, 1 / math.sqrt(d))
+    fin = np.nan_to_num(vn, nan=0, posinf=0, neginf=0)
+    ra, _ = S.prompt_attention(qn, kn, np.abs(fin), qs, ks, 1 / math.sqrt(d))
+    rows = int(qs[-1])
+    ro, ra, o, rl, lse = ro[:rows], ra[:rows], o[:rows], rl[:rows], lse[:rows]
+    assert np.array_equal(np.isnan(o), np.isnan(ro)) and np.array_equal(o[np.isinf(ro)], ro[np.isinf(ro)])
+    ok_ = np.isfinite(ro)
+    assert 0 < (~ok_).sum() < ok_.sum() and np.array_equal(np.isfinite(o), ok_)
+    assert (np.abs(o[ok_] - ro[ok_]) <= (2.0 ** -8 * (np.abs(ro) + ra) + 2.0 ** -12 * np.abs(fin).max())[ok_]).all()
+    big = np.abs(qn).sum(-1).max() * np.abs(kn).max() / math.sqrt(d)
+    assert (np.abs(lse - rl) <= 2.0 ** -17 * (1 + big)).all()
+
+
+def test_prompt_one_odd_value_costs_little():
+    """One value that is not finite near the end of a long prompt: its own
+    tile's last keys are summed another way, not the whole prompt before them."""
+    r = rng_of("pcost")
+    T, d = 8192, 128
+    q, k, v = (dev(r.normal(size=(T, h, d)), torch.bfloat16) for h in (8, 1, 1))
+    p = ssa.make_prompt_params(1, T, T, 8, 1, d)
+    st, o = dev([0, T], torch.int32), torch.empty_like(q)
+
+    def time():
+        best = math.inf
+        for _ in range(4):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            ssa.ssa_prompt_attn(p, q, k, v, st, st, o)
+            b.record()
+            ok()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    clean = time()
+    v[T - 40, 0, 3] = math.inf
+    assert time() < 4 * clean
+    assert torch.isinf(o[T - 40:, :, 3]).all() and torch.isfinite(o[:T - 40]).all()
+
+
 def test_prompt_without_any_keys():
     q = torch.ones(5, 8, 64, device="cuda", dtype=torch.bfloat16)
     kv = torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16)

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 1 ? kBlocks : 3) cache_attn_
     const int page = __shfl_sync(0xFFFFFFFFu, cur.page, b);
     const int key0 = __shfl_sync(0xFFFFFFFFu, cur.key0, b);
     const float ks = __shfl_sync(0xFFFFFFFFu, cur.ks, b);
-    const float vs = fmaxf(__shfl_sync(0xFFFFFFFFu, cur.vs, b), 1.17549435e-38f);
+    const float vs = fmaxf(__shfl_sync(0xFFFFFFFFu, cur.vs, b), 8.077935669463161e-28f);   // 2^-90: sums of its inverse stay finite
     const int lo = SEL ? __shfl_sync(0xFFFFFFFFu, cur.lo, b) : 0;
     const int st = i % C::STAGES;
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::STAGES) & 1, a.err, SITE_CACHE_FULL))) break;

@@ -783,6 +783,25 @@ def test_cache_attention_beside_a_page_of_far_larger_values():
         check_cache_rows(o, lse, q * factor, lens, table, codes, scale, page, sm_scale=2.0 ** -12)
 
 
+@pytest.mark.parametrize("low", [0.0, 2.0 ** -126, 2.0 ** -40])
+def test_cache_attention_over_pages_of_zeros(low):
+    """Pages of zero codes, with scales of zero too (a pool as it was allocated):
+    their keys count in the softmax like any other."""
+    r = rng_of("zeros", low)
+    d, page, lens = 128, 64, [1000, 3, 700]
+    table, codes, scale, q, _ = cache_case(r, lens, 1, 2, 4, d, page)
+    codes[:], scale[:] = 0, low
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page)
+    assert not o.any()
+    assert (np.abs(f64(lse)[:, 0] - np.log(lens)[:, None]) <= 2.0 ** -16).all()
+    codes[1, table[0, 5], :, 7] = S.to_e4m3(np.arange(-64, 64) * 1.0)       # one page holds something
+    scale[1, table[0, 5]] = 2.0 ** -3
+    o, lse, _ = run_cache(q, lens, table, codes, scale, page)
+    assert (np.abs(f64(lse)[:, 0] - np.log(lens)[:, None]) <= 2.0 ** -16).all()
+    want = S.e4m3_values()[codes[1, table[0, 5], 0, 7]] / 8 / 1000
+    assert not o[1:].any() and (np.abs(f64(o)[0] - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("size", [2.0 ** 14, 2.0 ** 18, 2.0 ** 22, 2.0 ** 24, 2.0 ** 40])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_cache_attention_of_logits_past_float32_steps(size, sign):

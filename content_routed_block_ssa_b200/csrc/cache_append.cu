@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, 512 / (P * D / 8 / kKeep)) 
     float w[8];
     uint64_t phase[4];
     lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
-    at.phases(a.g.freq, sub, phase);
+    at.warp_phases<D>(a.g.freq, is_k ? a.rot : 0, sub, phase);
     for (int h = h0 + warp; h < h1; h += THREADS / 32) append_head<T, D, P>(a, u, is_k, h, page, at, w, phase);
     return;
   }
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(P * D / 8 / kKeep, 512 / (P * D / 8 / kKeep)) 
   Angles angles[KEEP];
   if (is_k) {
     uint64_t phase[4];
-    at.phases(a.g.freq, sub, phase);
+    at.warp_phases<D>(a.g.freq, is_k ? a.rot : 0, sub, phase);
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
       angles[k].set<sizeof(T) == 4>(at, phase, u.pos0 + min(row + k * ROWS, u.n - 1), a.mscale);
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(256) append_few_kernel(const AppendCfg a) {
   float w[8];
   uint64_t phase[4];
   lane_weights(is_k && a.norm ? a.g.k_weight : nullptr, at, w);
-  at.phases(a.g.freq, sub, phase);
+  at.warp_phases<D>(a.g.freq, is_k ? a.rot : 0, sub, phase);
   float x[8], f = 1.f;
   const auto value = [&](int i0) {
     const int i = min(i0 + row, u.n - 1);

@@ -66,12 +66,8 @@ struct LaneDims {
     a = rotated && half ? 4 * sub : 8 * sub;
     b = rotated && half ? 4 * sub + rot / 2 : 8 * sub + 4;
   }
-  // The lane's four phases: pairs (a + i, b + i), or (a, a + 1), (a + 2, a + 3), (b, b + 1), (b + 2, b + 3).
-  __device__ __forceinline__ void phases(const double* freq, int sub, uint64_t (&phase)[4]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) phase[i] = rotated ? phase_of(__ldg(freq + 4 * sub + i)) : 0;
-  }
-  // The same, each computed once per block (every thread calls).
+  // The lane's four phases: pairs (a + i, b + i), or (a, a + 1), (a + 2, a + 3), (b, b + 1), (b + 2, b + 3);
+  // each computed once per block (every thread calls),
   __device__ __forceinline__ void block_phases(const double* freq, int rot, uint64_t (&all)[64], int sub,
                                                uint64_t (&phase)[4]) const {
     if (static_cast<int>(threadIdx.x) < rot / 2) all[threadIdx.x] = phase_of(__ldg(freq + threadIdx.x));
@@ -79,7 +75,7 @@ struct LaneDims {
 #pragma unroll
     for (int i = 0; i < 4; ++i) phase[i] = rotated ? all[4 * sub + i] : 0;
   }
-  // The same for a head of D dims, each computed once per warp (every lane calls).
+  // or, for a head of D dims, once per warp (every lane calls).
   template <int D>
   __device__ __forceinline__ void warp_phases(const double* freq, int rot, int sub, uint64_t (&phase)[4]) const {
     constexpr int N = D / 64;   // phases computed by a lane

@@ -9,7 +9,7 @@
 // copies of its own, so no warp waits for another until the end.  The products
 // are small against the bytes (2 G flops per byte): the kernel is bound by
 // reading codes (64 sequences of up to 16K tokens, 32 heads on 8, d = 128: 224
-// to 243 us by the box, 85 to 91% of the copy rate), and the instructions per
+// to 248 us by the box, 81 to 90% of the copy rate), and the instructions per
 // code decide whether it keeps up:
 //
 //  * the keys and the value dims are the M = 16 rows of the m16n8k16 products

@@ -8,7 +8,7 @@
 //
 // Two kernels (see run_rope): with many tokens each warp streams pieces of 2 KB
 // of neighbouring heads through shared memory by bulk copies, in and out, two
-// loads ahead (128K tokens of 40 heads, d = 128, bf16: 449 to 457 us, 90% of the
+// loads ahead (128K tokens of 40 heads, d = 128, bf16: 447 to 450 us, 91% of the
 // copy rate; straight from registers 508 at best); with few, the heads of a
 // token are spread over several warps that load straight to registers, which
 // starts sooner.

@@ -127,7 +127,7 @@ def used_blocks(row, pos, page):
 
 
 def cache_attention(q, table, kv_len, page, codes_k, codes_v, scale_k, scale_v, scale, block_idx=None, window=0):
-    """q [n, n_q, h_q, d]; returns (o, lse, largest sum of p |v| per row)."""
+    """q [n, n_q, h_q, d]; returns (o, lse)."""
     n, n_q, h_q, d = q.shape
     n_pages, h_kv = scale_k.shape
     G = h_q // h_kv

@@ -589,6 +589,9 @@ SSA_API size_t ssa_cache_attn_workspace_size(const ssa_cache_attn_params* p);
  * the second product as float16: a key's probability times its page's value
  * scale keeps 11 bits down to 2^-29 of the row's largest such product and
  * leaves O below 2^-40 of it (and lse below 2^-141).
+ * Queries enter the first product as float16 too, scaled by a power of two
+ * per row: exact down to 2^-29 of a row's largest element, left out below
+ * 2^-40 of it.
  * Meant for few new tokens (decode, drafts): with topk = 0 every 16 rows of
  * tokens x query heads of a kv-head read the sequence's cache once.
  *   Q          device [n_seq, n_q, h_q, d] bf16
